@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "../../include/externd.h"
+#include "int8_internal.h"
 #include "internal.h"
 
 namespace {
@@ -17,6 +18,29 @@ bool sizes_ok(int64_t m, int64_t n) {
   return m >= 1 && n >= 1 && m <= (int64_t)1 << 30 && n <= (int64_t)1 << 30 &&
          m * n < ((int64_t)1 << 31);
 }
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+bool float_type(int type) { return type == EXTERND_F32 || type == EXTERND_F16 || type == EXTERND_BF16; }
+
+bool float_matrix_ok(const void* p, int type, int64_t ld, int64_t cols) {
+  return p && float_type(type) && ((uintptr_t)p & (type == EXTERND_F32 ? 3u : 1u)) == 0 && ld >= cols &&
+         ld <= (int64_t)1 << 40;
+}
+
+bool bytes_matrix_ok(const void* p, int64_t ld, int64_t cols) {
+  return p && aligned16(p) && ld >= cols && ld % 16 == 0 && ld <= (int64_t)1 << 40;
+}
+
+// activations of an 8-bit product: floating point, or 8 bits with scales
+bool activations_ok(const void* X, int xtype, int64_t ldx, const float* xscale, int64_t n) {
+  if (xtype != EXTERND_I8) return float_matrix_ok(X, xtype, ldx, n);
+  return bytes_matrix_ok(X, ldx, n) && xscale && aligned4(xscale);
+}
+
+bool inner_ok(int64_t n) { return n >= 1 && n <= EXTERND_I8_MAX_INNER; }
+bool out_ok(int64_t m) { return m >= 1 && m <= EXTERND_I8_MAX_OUT; }
+bool rows_ok(int64_t r) { return r >= 0 && r <= EXTERND_I8_MAX_ROWS; }
 
 }  // namespace
 
@@ -138,6 +162,64 @@ int externd_ternary_apply(const uint32_t* packed_B, const uint32_t* packed_C, co
   if (nb < 1 || nb > 65536 || nb * (m > n ? m : n) >= ((int64_t)1 << 31))
     return EXTERND_ERR_INVALID_ARG;
   return externd::ternary_apply(packed_B, packed_C, D, m, n, k, X, nb, Y, (cudaStream_t)stream);
+}
+
+int externd_quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8_t* Q,
+                          int64_t ldq, float* scale, externd_stream_t stream) {
+  if (!rows_ok(rows) || !inner_ok(n) || !float_type(type)) return EXTERND_ERR_INVALID_ARG;
+  if (rows == 0) return EXTERND_OK;
+  if (!float_matrix_ok(X, type, ldx, n) || !bytes_matrix_ok(Q, ldq, n) || !scale || !aligned4(scale))
+    return EXTERND_ERR_INVALID_ARG;
+  return externd::i8::quantize_rows(X, type, ldx, rows, n, Q, ldq, scale, nullptr, nullptr,
+                                    (cudaStream_t)stream);
+}
+
+int externd_matmul_i8(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W,
+                      int64_t ldw, const float* wscale, const float* bias, int64_t rows, int64_t n,
+                      int64_t m, void* Y, int ytype, int64_t ldy, externd_stream_t stream) {
+  if (!rows_ok(rows) || !inner_ok(n) || !out_ok(m) || !float_type(ytype) ||
+      (xtype != EXTERND_I8 && !float_type(xtype)))
+    return EXTERND_ERR_INVALID_ARG;
+  if (!bytes_matrix_ok(W, ldw, n) || !wscale || !aligned4(wscale) || (bias && !aligned4(bias)))
+    return EXTERND_ERR_INVALID_ARG;
+  if (rows == 0) return EXTERND_OK;
+  if (!activations_ok(X, xtype, ldx, xscale, n) || !float_matrix_ok(Y, ytype, ldy, m))
+    return EXTERND_ERR_INVALID_ARG;
+  return externd::i8::matmul(X, xtype, ldx, xscale, W, ldw, wscale, bias, rows, n, m, Y, ytype, ldy,
+                             (cudaStream_t)stream);
+}
+
+int64_t externd_code_words(int64_t length) {
+  return out_ok(length) ? externd::i8::code_words(length) : 0;
+}
+
+int externd_pack_codes(const uint32_t* packed_B, const uint32_t* packed_C, const float* D,
+                       int64_t m, int64_t n, int64_t k, uint32_t* codes_B, uint32_t* codes_C,
+                       float* bound, externd_stream_t stream) {
+  if (!packed_B || !packed_C || !D || !codes_B || !codes_C || !bound) return EXTERND_ERR_INVALID_ARG;
+  if (!aligned4(packed_B) || !aligned4(packed_C) || !aligned4(D) || !aligned16(codes_B) ||
+      !aligned16(codes_C) || !aligned4(bound))
+    return EXTERND_ERR_INVALID_ARG;
+  if (!out_ok(m) || !inner_ok(n) || !inner_ok(k)) return EXTERND_ERR_INVALID_ARG;
+  return externd::i8::pack_codes(packed_B, packed_C, D, m, n, k, codes_B, codes_C, bound,
+                                 (cudaStream_t)stream);
+}
+
+int externd_ternary_apply_i8(const uint32_t* codes_B, const uint32_t* codes_C, const float* D,
+                             const float* bound, int64_t m, int64_t n, int64_t k, const void* X,
+                             int xtype, int64_t ldx, const float* xscale, int64_t rows, void* Y,
+                             int ytype, int64_t ldy, externd_stream_t stream) {
+  if (!codes_B || !codes_C || !D || !bound) return EXTERND_ERR_INVALID_ARG;
+  if (!aligned16(codes_B) || !aligned16(codes_C) || !aligned4(D) || !aligned4(bound))
+    return EXTERND_ERR_INVALID_ARG;
+  if (!rows_ok(rows) || !out_ok(m) || !inner_ok(n) || !inner_ok(k) || !float_type(ytype) ||
+      (xtype != EXTERND_I8 && !float_type(xtype)))
+    return EXTERND_ERR_INVALID_ARG;
+  if (rows == 0) return EXTERND_OK;
+  if (!activations_ok(X, xtype, ldx, xscale, n) || !float_matrix_ok(Y, ytype, ldy, m))
+    return EXTERND_ERR_INVALID_ARG;
+  return externd::i8::factors(codes_B, codes_C, D, bound, m, n, k, X, xtype, ldx, xscale, rows, Y,
+                              ytype, ldy, (cudaStream_t)stream);
 }
 
 int externd_release_cache(void) {

@@ -267,6 +267,9 @@ int launch_apply(ApArgs a, int G, size_t smem, cudaStream_t st) {
 std::mutex g_pool_mu;
 cudaMemPool_t g_pools[64] = {};
 
+}  // namespace
+
+// (also the scratch of the 8-bit products)
 cudaMemPool_t apply_pool(int dev) {
   cudaMemPool_t* const pools = g_pools;
   if (dev < 0 || dev >= 64) return nullptr;
@@ -287,8 +290,6 @@ cudaMemPool_t apply_pool(int dev) {
   }
   return pools[dev];
 }
-
-}  // namespace
 
 // Returns the memory the pools hold beyond what queued calls still use.
 int apply_trim_pools() {

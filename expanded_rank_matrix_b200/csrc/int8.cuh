@@ -1,0 +1,110 @@
+// Shared pieces of the 8-bit inference kernels (quantize_rows, matmul_i8,
+// pack_codes, ternary_apply_i8).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/externd.h"
+
+namespace externd {
+namespace i8 {
+
+// Packed ternary codes: a row of length L is code_words(L) 32-bit words of 16
+// two-bit fields each; entry 16 w + 4 s + b sits in bits 8 b + 6 - 2 s and
+// 8 b + 7 - 2 s of word w.  A field is the two's complement of its entry (01 =
+// +1, 11 = -1), so (word << 2 s) & 0xC0C0C0C0 is four consecutive entries as
+// signed bytes +-64: two instructions for four codes, and the factor 64
+// leaves the whole-number sums by an exact shift.  Rows are padded with zero
+// codes to 128 entries (32 bytes), the K step of the tensor-core kernel.
+__host__ __device__ constexpr int64_t code_words(int64_t len) { return (len + 127) / 128 * 8; }
+constexpr uint32_t kCodeMask = 0xC0C0C0C0u;
+constexpr int kCodeShift = 6;
+
+// Largest inner dimension: the sums of n products of 8-bit values and
+// 64 * (ternary) stay below 2^31, and those of 8-bit values and codes below
+// 2^24 (exact in fp32).
+constexpr int64_t kMaxInner = EXTERND_I8_MAX_INNER;
+
+// The 16-bit component sums: |h| <= 127 * 256, so both 8-bit planes of
+// h = 256 hi + lo (lo in -128 .. 127) fit.
+constexpr double kFullScale = 32512.0;
+
+// What the products write.
+enum Epilogue { kOutDense, kOutPlanes, kOutFactors };
+
+struct GemmArgs {
+  const int8_t* x;      // activations [rows][ldx] (kOutFactors: plane hi; plane lo at x + plane)
+  int64_t ldx;
+  int64_t plane;        // bytes between the two planes
+  const void* w;        // int8 [M][ldw], or codes [M][ldw words]
+  int64_t ldw;
+  const float* wscale;  // dense: scale of each output channel; planes: D
+  const float* bias;    // dense: [M] or null
+  const float* xscale;  // scale of each token
+  const float* z;       // scale of each token's component sums (planes, factors)
+  void* y;              // dense, factors: output; planes: plane hi (plane lo at y + plane)
+  int64_t ldy;
+  int ytype;
+  int rows, M, K;       // tokens, weight rows, inner dimension
+  int* status;
+  long long budget;
+};
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+__device__ __forceinline__ void store_out(void* y, int64_t at, int ytype, float v) {
+  if (ytype == EXTERND_BF16)
+    ((__nv_bfloat16*)y)[at] = __float2bfloat16_rn(v);
+  else if (ytype == EXTERND_F16)
+    ((__half*)y)[at] = __float2half_rn(v);
+  else
+    ((float*)y)[at] = v;
+}
+
+// x / s to the nearest whole number, ties to even, exactly: x * inv (inv =
+// fl(1 / s)) is within a few 2^-23 of the quotient, so its rounding q is the
+// answer or a neighbour; the remainder x - q s is a multiple of the smaller
+// operand's last place and below s, so the fused multiply-add returns it
+// without error and its comparison with s / 2 decides.  Valid for normal s
+// away from the ends of the range (safe_scale) and |x / s| < 2^16.
+__device__ __forceinline__ float nearest_quotient(float x, float s, float inv) {
+  float q = rintf(x * inv);
+  const float r = fmaf(-q, s, x);
+  const float twice = 2.f * fabsf(r);
+  if (twice > s || (twice == s && ((int)q & 1))) q += r > 0.f ? 1.f : -1.f;
+  return q;
+}
+__device__ __forceinline__ bool safe_scale(float s) { return s > 1e-30f && s < 1e30f; }
+// the same for any s > 0 (a quotient of two fp32 values cannot round onto a
+// half in fp64 without being one)
+__device__ __forceinline__ float nearest_quotient_slow(float x, float s) {
+  return (float)rint((double)x / (double)s);
+}
+
+// Component sum -> 16-bit value (0 for z = 0 or not finite).
+__device__ __forceinline__ int component_value(float p, float z, float inv, bool safe) {
+  float q;
+  if (safe) {
+    q = nearest_quotient(p, z, inv);
+  } else {
+    if (!(z > 0.f) || isinf(z)) return 0;
+    q = nearest_quotient_slow(p, z);
+  }
+  // (|p| <= rho sqrt(r) keeps |q| <= 32512; the clamp only tames a NaN or
+  // infinite D)
+  return (int)fminf(fmaxf(q, -32512.f), 32512.f);
+}
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+}  // namespace i8
+}  // namespace externd

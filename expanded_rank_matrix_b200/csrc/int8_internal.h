@@ -1,0 +1,28 @@
+// Internal interfaces of the 8-bit inference path.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "int8.cuh"
+
+namespace externd {
+namespace i8 {
+
+// Q, scale from X; with rho also z = fl(rho |q|_2 / 32512) of each row.
+int quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8_t* Q,
+                  int64_t ldq, float* scale, const float* rho, float* z, cudaStream_t st);
+int row_norms(const int8_t* Q, int64_t ldq, int64_t rows, int64_t n, const float* rho, float* z,
+              cudaStream_t st);
+int pack_codes(const uint32_t* pB, const uint32_t* pC, const float* D, int64_t m, int64_t n,
+               int64_t k, uint32_t* codes_B, uint32_t* codes_C, float* rho, cudaStream_t st);
+int skinny_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
+int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W, int64_t ldw,
+           const float* wscale, const float* bias, int64_t rows, int64_t n, int64_t m, void* Y,
+           int ytype, int64_t ldy, cudaStream_t st);
+int factors(const uint32_t* codes_B, const uint32_t* codes_C, const float* D, const float* rho,
+            int64_t m, int64_t n, int64_t k, const void* X, int xtype, int64_t ldx,
+            const float* xscale, int64_t rows, void* Y, int ytype, int64_t ldy, cudaStream_t st);
+
+}  // namespace i8
+}  // namespace externd

@@ -1,0 +1,293 @@
+// Quantising rows to 8 bits with one scale a row, and packing the ternary
+// factors into the two-bit codes that the 8-bit products read.
+//
+// quantize: a = max_j |x_j|, s = fl(a / 127), q_j = the whole number nearest
+// to x_j / s (exact, ties to even).  One pass: a group of threads holds its
+// row in registers between the maximum and the rounding, so the row is read
+// once and its 8-bit copy written once; HBM bandwidth is the bound.
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "int8.cuh"
+#include "int8_internal.h"
+#include "internal.h"
+
+namespace externd {
+namespace i8 {
+namespace {
+
+constexpr int kHeld = 8;  // 16-byte vectors of its row that a thread holds
+
+template <typename T>
+struct RowArgs {
+  const T* x;
+  int64_t ldx;
+  int8_t* q;
+  int64_t ldq;
+  float* scale;
+  const float* rho;  // with z: the factors' bound
+  float* z;          // scale of the row's component sums, or null
+  int64_t rows;
+  int n;
+  int* status;
+};
+
+// E elements at x[j ..] (zeros past n); VEC: every row starts 16-byte aligned
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_vec(const T* x, int j, int n, T (&v)[16 / sizeof(T)]) {
+  constexpr int E = 16 / sizeof(T);
+  if (VEC && j + E <= n) {
+    *(uint4*)v = __ldg((const uint4*)(x + j));
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = j + e < n ? x[j + e] : T(0.f);
+  }
+}
+
+// Sum or maximum over the G threads of a row group; every thread gets it.
+template <int G, bool MAX>
+__device__ __forceinline__ uint32_t group_reduce(uint32_t v, uint32_t* red) {
+  v = MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_add_sync(0xffffffffu, v);
+  if (G == 32) return v;
+  constexpr int W = G / 32;
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __syncthreads();
+  if (lane == 0) red[wid] = v;
+  __syncthreads();
+  v = lane < W ? red[(wid / W) * W + lane] : 0u;
+  return MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_add_sync(0xffffffffu, v);
+}
+
+// G threads a row; blockDim.x / G rows a CTA.
+template <typename T, int G, bool VEC>
+__global__ void __launch_bounds__(G > 256 ? G : 256) rows_kernel(const RowArgs<T> a) {
+  constexpr int E = 16 / sizeof(T);
+  __shared__ uint32_t red[32];
+  pdl_trigger();
+  const int tid = threadIdx.x % G;
+  const int64_t row0 = (int64_t)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
+  const bool live = row0 < a.rows;
+  const int64_t row = live ? row0 : a.rows - 1;  // (whole warps take part in the reductions)
+  const T* x = a.x + row * a.ldx;
+  T v[kHeld][E];
+  // magnitudes as the bit patterns of non-negative floats, which order like
+  // integers; a NaN is above infinity, so one comparison finds either
+  uint32_t top = 0u;
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) {
+    const int j = (h * G + tid) * E;
+    if (j < a.n) {
+      load_vec<T, VEC>(x, j, a.n, v[h]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(to_f32(v[h][e])) & 0x7fffffffu);
+    }
+  }
+  for (int j = (kHeld * G + tid) * E; j < a.n; j += G * E) {
+    T u[E];
+    load_vec<T, VEC>(x, j, a.n, u);
+#pragma unroll
+    for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(to_f32(u[e])) & 0x7fffffffu);
+  }
+  top = group_reduce<G, true>(top, red);
+  const bool finite = top < 0x7f800000u;
+  const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.f) : __uint_as_float(0x7fc00000u);
+  const bool safe = safe_scale(s);
+  const float inv = safe ? __fdiv_rn(1.f, s) : 0.f;
+  if (live && tid == 0) {
+    a.scale[row] = s;
+    if (!finite) atomicCAS(a.status, 0, EXTERND_ERR_NONFINITE);
+  }
+  int8_t* q = a.q + row * a.ldq;
+  uint32_t squares = 0u;
+  auto emit = [&](int j, const T (&u)[E]) {
+    uint32_t packed[E / 4];
+#pragma unroll
+    for (int p = 0; p < E / 4; ++p) {
+      uint32_t word = 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = to_f32(u[4 * p + e]);
+        // (a subnormal scale may put x / s past 127: the clamp keeps 8 bits)
+        const float r = safe ? nearest_quotient(f, s, inv)
+                        : s > 0.f ? fminf(fmaxf(nearest_quotient_slow(f, s), -127.f), 127.f)
+                                  : 0.f;
+        word |= ((uint32_t)(int)r & 0xffu) << (8 * e);
+      }
+      packed[p] = word;
+      squares = __dp4a((int)word, (int)word, (int)squares);
+    }
+    if (!live) return;
+    if (j + E <= a.n) {
+      if (E == 8)
+        *(uint2*)(q + j) = make_uint2(packed[0], packed[E / 4 - 1]);
+      else
+        *(uint32_t*)(q + j) = packed[0];
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (j + e < a.n) q[j + e] = (int8_t)(packed[e / 4] >> (8 * (e & 3)));
+    }
+  };
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) {
+    const int j = (h * G + tid) * E;
+    if (j < a.n) emit(j, v[h]);
+  }
+  for (int j = (kHeld * G + tid) * E; j < a.n; j += G * E) {
+    T u[E];
+    load_vec<T, VEC>(x, j, a.n, u);
+    emit(j, u);
+  }
+  if (a.z) {
+    squares = group_reduce<G, false>(squares, red);
+    if (live && tid == 0)
+      a.z[row] = (float)((double)__ldg(a.rho) * sqrt((double)squares) / kFullScale);
+  }
+}
+
+// z of rows that are already quantised: one warp a row.
+__global__ void __launch_bounds__(256) row_norm_kernel(const int8_t* __restrict__ q, int64_t ldq,
+                                                       int64_t rows, int n,
+                                                       const float* __restrict__ rho,
+                                                       float* __restrict__ z) {
+  pdl_trigger();
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 31;
+  const int8_t* x = q + row * ldq;
+  int sum = 0;
+  for (int j = lane * 16; j < n; j += 512) {
+    if (j + 16 <= n) {
+      const int4 v = __ldg((const int4*)(x + j));
+      sum = __dp4a(v.x, v.x, sum);
+      sum = __dp4a(v.y, v.y, sum);
+      sum = __dp4a(v.z, v.z, sum);
+      sum = __dp4a(v.w, v.w, sum);
+    } else {
+      for (int e = j; e < n; ++e) sum += (int)x[e] * (int)x[e];
+    }
+  }
+  const uint32_t total = __reduce_add_sync(0xffffffffu, (uint32_t)sum);
+  if (lane == 0) z[row] = (float)((double)__ldg(rho) * sqrt((double)total) / kFullScale);
+}
+
+template <typename T, int G, bool VEC>
+int launch_rows_g(const RowArgs<T>& a, cudaStream_t st) {
+  constexpr int threads = G > 256 ? G : 256;
+  constexpr int per = threads / G;
+  const int64_t grid = (a.rows + per - 1) / per;
+  if (grid > 2147483647LL) return EXTERND_ERR_INVALID_ARG;
+  rows_kernel<T, G, VEC><<<(unsigned)grid, threads, 0, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return EXTERND_ERR_CUDA;
+  return EXTERND_OK;
+}
+
+template <typename T>
+int launch_rows(const RowArgs<T>& a, cudaStream_t st) {
+  const bool vec = ((uintptr_t)a.x & 15) == 0 && (a.ldx * (int64_t)sizeof(T)) % 16 == 0;
+  // a warp holds 4 KB of a row: longer rows take a CTA each
+  const bool wide = a.n * (int64_t)sizeof(T) > 32 * kHeld * 16;
+  if (wide) return vec ? launch_rows_g<T, 256, true>(a, st) : launch_rows_g<T, 256, false>(a, st);
+  return vec ? launch_rows_g<T, 32, true>(a, st) : launch_rows_g<T, 32, false>(a, st);
+}
+
+template <typename T>
+int rows_of(const void* x, int64_t ldx, int64_t rows, int64_t n, int8_t* q, int64_t ldq,
+            float* scale, const float* rho, float* z, cudaStream_t st) {
+  RowArgs<T> a = {};
+  a.x = (const T*)x; a.ldx = ldx; a.q = q; a.ldq = ldq; a.scale = scale; a.rho = rho; a.z = z;
+  a.rows = rows; a.n = (int)n;
+  a.status = status_word_ptr();
+  if (!a.status) return EXTERND_ERR_CUDA;
+  return launch_rows<T>(a, st);
+}
+
+// ---- packing the factors ----
+
+// Codes of B: [m][words], from component-major planes: a thread takes 16
+// components of one row (its warp reads one word of each component's planes).
+__global__ void __launch_bounds__(256) pack_b_kernel(const uint32_t* __restrict__ pB, int m, int k,
+                                                     int words, uint32_t* __restrict__ out) {
+  const int Wm = (m + 31) >> 5;
+  const int i = blockIdx.x * 32 + (threadIdx.x & 31);
+  const int w = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (i >= m || w >= words) return;
+  const int bit = i & 31;
+  uint32_t v = 0u;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int c = 16 * w + e;
+    if (c < k) {
+      const uint32_t* p = pB + (int64_t)c * 2 * Wm + (i >> 5);
+      const uint32_t mk = (__ldg(p) >> bit) & 1u, sg = (__ldg(p + Wm) >> bit) & 1u;
+      v |= (mk * (1u + 2u * sg)) << (8 * (e & 3) + 6 - 2 * (e >> 2));
+    }
+  }
+  out[(int64_t)i * words + w] = v;
+}
+
+// Codes of C: [k][words], and rho = max_c |D_c| sqrt(nnz_c).  A warp a
+// component.  rho rounds to fp32 before the maximum (the rounding is
+// monotone), as a bit pattern, where a NaN D comes out on top.
+__global__ void __launch_bounds__(256) pack_c_kernel(const uint32_t* __restrict__ pC,
+                                                     const float* __restrict__ D, int n, int k,
+                                                     int words, uint32_t* __restrict__ out,
+                                                     float* __restrict__ rho) {
+  const int Wn = (n + 31) >> 5;
+  const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (c >= k) return;
+  const uint32_t* p = pC + (int64_t)c * 2 * Wn;
+  uint32_t nnz = 0u;
+  for (int w = lane; w < words; w += 32) {
+    uint32_t v = 0u;
+    if ((w >> 1) < Wn) {
+      const uint32_t mk = __ldg(p + (w >> 1)) >> (16 * (w & 1));
+      const uint32_t sg = __ldg(p + Wn + (w >> 1)) >> (16 * (w & 1));
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t mb = (mk >> e) & 1u, sb = (sg >> e) & 1u;
+        v |= (mb * (1u + 2u * sb)) << (8 * (e & 3) + 6 - 2 * (e >> 2));
+        nnz += mb;
+      }
+    }
+    out[(int64_t)c * words + w] = v;
+  }
+  nnz = __reduce_add_sync(0xffffffffu, nnz);
+  if (lane == 0) {
+    const float r = (float)(fabs((double)D[c]) * sqrt((double)nnz));
+    atomicMax((unsigned*)rho, __float_as_uint(r) & 0x7fffffffu);
+  }
+}
+
+}  // namespace
+
+int quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8_t* Q,
+                  int64_t ldq, float* scale, const float* rho, float* z, cudaStream_t st) {
+  if (type == EXTERND_BF16)
+    return rows_of<__nv_bfloat16>(X, ldx, rows, n, Q, ldq, scale, rho, z, st);
+  if (type == EXTERND_F16) return rows_of<__half>(X, ldx, rows, n, Q, ldq, scale, rho, z, st);
+  return rows_of<float>(X, ldx, rows, n, Q, ldq, scale, rho, z, st);
+}
+
+int row_norms(const int8_t* Q, int64_t ldq, int64_t rows, int64_t n, const float* rho, float* z,
+              cudaStream_t st) {
+  const int64_t grid = (rows + 7) / 8;
+  row_norm_kernel<<<(unsigned)grid, 256, 0, st>>>(Q, ldq, rows, (int)n, rho, z);
+  return cudaGetLastError() == cudaSuccess ? EXTERND_OK : EXTERND_ERR_CUDA;
+}
+
+int pack_codes(const uint32_t* pB, const uint32_t* pC, const float* D, int64_t m, int64_t n,
+               int64_t k, uint32_t* codes_B, uint32_t* codes_C, float* rho, cudaStream_t st) {
+  const int wb = (int)code_words(k), wc = (int)code_words(n);
+  if (cudaMemsetAsync(rho, 0, sizeof(float), st) != cudaSuccess) return EXTERND_ERR_CUDA;
+  pack_b_kernel<<<dim3((unsigned)((m + 31) / 32), (unsigned)((wb + 7) / 8)), 256, 0, st>>>(
+      pB, (int)m, (int)k, wb, codes_B);
+  pack_c_kernel<<<(unsigned)((k + 7) / 8), 256, 0, st>>>(pC, D, (int)n, (int)k, wc, codes_C, rho);
+  return cudaGetLastError() == cudaSuccess ? EXTERND_OK : EXTERND_ERR_CUDA;
+}
+
+}  // namespace i8
+}  // namespace externd

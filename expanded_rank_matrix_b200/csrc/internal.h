@@ -76,6 +76,7 @@ int tc_contract_rtu(const float* R, int m, int n, const unsigned long long* Um,
                     const unsigned long long* Us, const unsigned char* Bop, int bb, const TcPlan* p,
                     int klen, int splits, float* Qp, long long budget, cudaStream_t st);
 int block_release_graphs();
+cudaMemPool_t apply_pool(int dev);  // the inference scratch pool of a device
 int apply_trim_pools();
 int seq_decompose_with_scratch(const SeqHostArgs& h, void* scratch, size_t scratch_bytes,
                                cudaStream_t st);

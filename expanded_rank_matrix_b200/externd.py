@@ -35,7 +35,9 @@ MAX_SWEEPS = 64
 EXPORTS = ("externd_rank", "externd_decompose", "externd_decompose_ex", "externd_decompose_traced",
            "externd_reconstruct", "externd_sync_status", "externd_decompose_noalloc",
            "externd_decompose_block_traced", "externd_rank_for_energy",
-           "externd_ternary_apply", "externd_probe_read_bandwidth", "externd_release_cache")
+           "externd_ternary_apply", "externd_probe_read_bandwidth", "externd_release_cache",
+           "externd_quantize_rows", "externd_matmul_i8", "externd_code_words",
+           "externd_pack_codes", "externd_ternary_apply_i8")
 
 _lib = None
 _vp = ctypes.c_void_p
@@ -83,6 +85,18 @@ def load(path: str = LIB_PATH):
     L.externd_rank_for_energy.restype = ctypes.c_int
     L.externd_ternary_apply.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp]
     L.externd_ternary_apply.restype = ctypes.c_int
+    L.externd_quantize_rows.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _vp]
+    L.externd_quantize_rows.restype = ctypes.c_int
+    L.externd_matmul_i8.argtypes = [_vp, ctypes.c_int, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64,
+                                    _i64, _vp, ctypes.c_int, _i64, _vp]
+    L.externd_matmul_i8.restype = ctypes.c_int
+    L.externd_code_words.argtypes = [_i64]
+    L.externd_code_words.restype = _i64
+    L.externd_pack_codes.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp]
+    L.externd_pack_codes.restype = ctypes.c_int
+    L.externd_ternary_apply_i8.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, ctypes.c_int,
+                                           _i64, _vp, _i64, _vp, ctypes.c_int, _i64, _vp]
+    L.externd_ternary_apply_i8.restype = ctypes.c_int
     L.externd_probe_read_bandwidth.argtypes = [ctypes.c_int, _vp, _i64, ctypes.c_int,
                                                ctypes.POINTER(ctypes.c_int64), _vp]
     L.externd_probe_read_bandwidth.restype = ctypes.c_int
@@ -297,6 +311,231 @@ def apply(f: Factors, X: torch.Tensor, stream: Optional[torch.cuda.Stream] = Non
     Y = torch.empty((X2.shape[0], f.m), dtype=torch.float32, device=X.device)
     apply_into(f, X2, Y, stream)
     return Y.reshape(*X.shape[:-1], f.m)
+
+
+# --- 8-bit inference ---------------------------------------------------------
+
+I8_MAX_INNER = 131071
+I8_MAX_OUT = 1 << 24
+
+F32, F16, BF16, I8 = 0, 1, 2, 3
+_TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+
+
+@dataclass
+class Quantized:
+    """Rows in 8 bits with one scale a row: row i stands for q[i] * scale[i].
+    q is int8 [rows, n] whose rows start on 16-byte boundaries and hold
+    readable storage up to the next one (as quantize_rows allocates it);
+    scale is fp32 [rows].  Any other int8 matrix is copied into that form
+    when it is used."""
+    q: torch.Tensor
+    scale: torch.Tensor
+
+
+@dataclass
+class FactorCodes:
+    """Factors laid out for apply_i8 (pack_codes): two-bit codes, B row by row
+    and C component by component, D, and the bound of the component sums."""
+    codes_B: torch.Tensor  # int32 view of uint32 [m, code_words(k)]
+    codes_C: torch.Tensor  # [k, code_words(n)]
+    D: torch.Tensor        # fp32 [k]
+    bound: torch.Tensor    # fp32 [1]
+    m: int
+    n: int
+
+    @property
+    def k(self) -> int:
+        return int(self.D.shape[0])
+
+
+def code_words(length: int) -> int:
+    """32-bit words of one row of packed ternary codes."""
+    return int(load().externd_code_words(length))
+
+
+class _On:
+    """Makes a tensor's device, and a given stream, the current ones, so that
+    allocations and copies made inside belong to the stream of the launch."""
+
+    def __init__(self, index: int, stream: Optional[torch.cuda.Stream]):
+        if stream is not None and stream.device_index != index:
+            raise ValueError("the stream belongs to another device than the tensors")
+        self._ctx = None
+        if stream is not None:
+            self._ctx = torch.cuda.stream(stream)
+        elif index != torch.cuda.current_device():
+            self._ctx = torch.cuda.device(index)
+        self.index = index
+
+    def __enter__(self) -> int:
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        return False
+
+
+def _device_index(t: torch.Tensor, *others) -> int:
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    index = t.get_device()
+    for o in others:
+        if o is not None and (not o.is_cuda or o.get_device() != index):
+            raise ValueError("expected tensors on one CUDA device")
+    return index
+
+
+def _matrix(X: torch.Tensor) -> torch.Tensor:
+    """X [..., n] as a matrix of rows, without a copy where its rows lie at
+    one distance and their elements side by side."""
+    if X.dim() == 0:
+        raise ValueError("expected at least one dimension")
+    M = X if X.dim() == 2 else X.reshape(-1, X.shape[-1])
+    rows, n = M.shape
+    if (n > 1 and M.stride(1) != 1) or (rows > 1 and M.stride(0) < n):
+        M = M.contiguous()
+    return M
+
+
+def _ld(M: torch.Tensor) -> int:
+    # (the stride of a single row means nothing)
+    return M.stride(0) if M.shape[0] > 1 else max(M.shape[1], 1)
+
+
+def _aligned_rows(q: torch.Tensor) -> torch.Tensor:
+    """An int8 matrix whose rows start on 16-byte boundaries within storage
+    that holds every row up to the next one: q itself, or a copy."""
+    if q.dtype != torch.int8 or q.dim() != 2:
+        raise ValueError("expected a 2-D int8 tensor")
+    rows, n = q.shape
+    if rows == 0 or n == 0:
+        return q
+    ld = q.stride(0) if rows > 1 else (n + 15) // 16 * 16
+    end = q.storage_offset() + (rows - 1) * ld + (n + 15) // 16 * 16
+    if ((n == 1 or q.stride(1) == 1) and q.data_ptr() % 16 == 0 and ld % 16 == 0 and ld >= n
+            and end <= q.untyped_storage().nbytes()):
+        return q
+    out = torch.empty((rows, (n + 15) // 16 * 16), dtype=torch.int8, device=q.device)[:, :n]
+    out.copy_(q)
+    return out
+
+
+def _ld_bytes(q: torch.Tensor) -> int:
+    return q.stride(0) if q.shape[0] > 1 else (q.shape[1] + 15) // 16 * 16
+
+
+def _vector(v: torch.Tensor, length: int, what: str) -> torch.Tensor:
+    if v.dtype != torch.float32 or v.dim() != 1 or v.shape[0] != length:
+        raise ValueError(f"{what} must be fp32 [{length}]")
+    return v.contiguous()
+
+
+def quantize_rows(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> Quantized:
+    """Symmetric 8-bit quantisation of the rows of X [..., n] (fp32, fp16 or
+    bf16) with one scale a row (externd_quantize_rows): tokens of activations,
+    output channels of a weight matrix."""
+    if X.dtype not in _TYPES:
+        raise ValueError("X must be fp32, fp16 or bf16")
+    with _On(_device_index(X), stream) as st:
+        M = _matrix(X)
+        rows, n = M.shape
+        ldq = (n + 15) // 16 * 16
+        q = torch.empty((rows, ldq), dtype=torch.int8, device=X.device)
+        scale = torch.empty(rows, dtype=torch.float32, device=X.device)
+        rc = load().externd_quantize_rows(M.data_ptr(), _TYPES[X.dtype], _ld(M), rows, n,
+                                          q.data_ptr(), ldq, scale.data_ptr(), st)
+    if rc != OK:
+        raise ExterndError(rc, "externd_quantize_rows")
+    return Quantized(q if ldq == n else q[:, :n], scale)
+
+
+def _activations(X, n: int, out_dtype):
+    """(matrix, scales, type, row distance, leading shape, output type)."""
+    if isinstance(X, Quantized):
+        q = _aligned_rows(X.q)
+        s = _vector(X.scale, q.shape[0], "scale")
+        if q.shape[1] != n:
+            raise ValueError(f"X must have {n} columns")
+        return q, s, I8, _ld_bytes(q), (q.shape[0],), out_dtype or torch.float32
+    if X.dtype not in _TYPES:
+        raise ValueError("X must be fp32, fp16, bf16 or Quantized")
+    M = _matrix(X)
+    if M.shape[1] != n:
+        raise ValueError(f"X must have {n} columns")
+    return M, None, _TYPES[X.dtype], _ld(M), X.shape[:-1], out_dtype or X.dtype
+
+
+def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=None,
+              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """X W^T (+ bias) with 8-bit operands and whole-number sums, one scale for
+    each token and each output channel (externd_matmul_i8).  X: [..., n] fp32,
+    fp16 or bf16, quantised within the call, or Quantized rows (shared by
+    several products).  The output is [..., m] of out_dtype (default: X's
+    type; fp32 for Quantized)."""
+    x = X.q if isinstance(X, Quantized) else X
+    with _On(_device_index(x, X.scale if isinstance(X, Quantized) else None, W.q, W.scale, bias),
+             stream) as st:
+        w = _aligned_rows(W.q)
+        m, n = w.shape
+        ws = _vector(W.scale, m, "scale")
+        b = None if bias is None else _vector(bias, m, "bias")
+        M, s, xtype, ldx, lead, dt = _activations(X, n, out_dtype)
+        if dt not in _TYPES:
+            raise ValueError("out_dtype must be fp32, fp16 or bf16")
+        rows = M.shape[0]
+        Y = torch.empty((*lead, m), dtype=dt, device=M.device)
+        rc = load().externd_matmul_i8(M.data_ptr(), xtype, ldx, None if s is None else s.data_ptr(),
+                                      w.data_ptr(), _ld_bytes(w), ws.data_ptr(),
+                                      None if b is None else b.data_ptr(), rows, n, m,
+                                      Y.data_ptr(), _TYPES[dt], m, st)
+    if rc != OK:
+        raise ExterndError(rc, "externd_matmul_i8")
+    return Y
+
+
+def pack_codes(f: Factors, stream: Optional[torch.cuda.Stream] = None) -> FactorCodes:
+    """Lays factors out once for apply_i8 (externd_pack_codes).  The factors
+    of a decomposition, or some of its components (truncate)."""
+    with _On(_device_index(f.D, f.packed_B, f.packed_C), stream) as st:
+        dev, k = f.D.device, f.k
+        D = f.D.contiguous()
+        pB, pC = f.packed_B.contiguous(), f.packed_C.contiguous()
+        if pB.shape != (k, 2, words(f.m)) or pC.shape != (k, 2, words(f.n)):
+            raise ValueError("packed factors and D do not belong together")
+        if (pB.dtype, pC.dtype, D.dtype) != (torch.int32, torch.int32, torch.float32):
+            raise ValueError("packed factors must be int32 and D fp32")
+        cB = torch.empty((f.m, code_words(k)), dtype=torch.int32, device=dev)
+        cC = torch.empty((k, code_words(f.n)), dtype=torch.int32, device=dev)
+        bound = torch.empty(1, dtype=torch.float32, device=dev)
+        rc = load().externd_pack_codes(pB.data_ptr(), pC.data_ptr(), D.data_ptr(), f.m, f.n, k,
+                                       cB.data_ptr(), cC.data_ptr(), bound.data_ptr(), st)
+    if rc != OK:
+        raise ExterndError(rc, "externd_pack_codes")
+    return FactorCodes(cB, cC, D, bound, f.m, f.n)
+
+
+def apply_i8(c: FactorCodes, X, out_dtype=None,
+             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """X (B diag(D) C)^T on 8-bit activations, from the packed codes
+    (externd_ternary_apply_i8).  X and out_dtype as for matmul_i8."""
+    x = X.q if isinstance(X, Quantized) else X
+    with _On(_device_index(x, X.scale if isinstance(X, Quantized) else None, c.D, c.codes_B,
+                           c.codes_C, c.bound), stream) as st:
+        M, s, xtype, ldx, lead, dt = _activations(X, c.n, out_dtype)
+        if dt not in _TYPES:
+            raise ValueError("out_dtype must be fp32, fp16 or bf16")
+        Y = torch.empty((*lead, c.m), dtype=dt, device=M.device)
+        rc = load().externd_ternary_apply_i8(
+            c.codes_B.data_ptr(), c.codes_C.data_ptr(), c.D.data_ptr(), c.bound.data_ptr(), c.m,
+            c.n, c.D.shape[0], M.data_ptr(), xtype, ldx, None if s is None else s.data_ptr(),
+            M.shape[0], Y.data_ptr(), _TYPES[dt], c.m, st)
+    if rc != OK:
+        raise ExterndError(rc, "externd_ternary_apply_i8")
+    return Y
 
 
 PROBE_SMEM = 0

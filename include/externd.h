@@ -257,6 +257,125 @@ int externd_ternary_apply(const uint32_t* packed_B, const uint32_t* packed_C, co
                           externd_stream_t stream);
 
 /*
+ * 8-bit inference: rows quantised to 8 bits with one scale a row, and the two
+ * projection products on them, from dense 8-bit weights and from the ternary
+ * factors.  The pages have no counterpart; the products are the batched forms
+ * next to externd_ternary_apply, on the tensor cores.
+ *
+ * Element types of activations and outputs (EXTERND_I8: already quantised
+ * activations, with their scales).
+ */
+#define EXTERND_F32 0
+#define EXTERND_F16 1
+#define EXTERND_BF16 2
+#define EXTERND_I8 3
+/* Largest inner dimension (n; k of the factored product) and largest output
+ * dimension: every sum of 8-bit products below stays a 32-bit whole number. */
+#define EXTERND_I8_MAX_INNER 131071
+#define EXTERND_I8_MAX_OUT (1 << 24)
+#define EXTERND_I8_MAX_ROWS (1 << 30)
+
+/*
+ * externd_quantize_rows -- symmetric 8-bit quantisation, one scale a row
+ * (tokens of activations, output channels of weights):
+ *   a = max_j |x_j|,  scale = fl32(a / 127),
+ *   q_j = the whole number nearest to x_j / scale, ties to even (0 if the
+ *         scale is 0; at most 127 in magnitude).
+ * A row with an infinity or a NaN gets scale NaN and q = 0 (so products with
+ * it are NaN, and no other row is touched) and raises EXTERND_ERR_NONFINITE
+ * in the status word.
+ *
+ *   X      [rows][ldx] of `type` (EXTERND_F32 / _F16 / _BF16), aligned to its
+ *          element, ldx >= n elements between rows.
+ *   rows   0 .. EXTERND_I8_MAX_ROWS (0: nothing is done).
+ *   n      1 .. EXTERND_I8_MAX_INNER.
+ *   Q      [rows][ldq] int8 out, 16-byte aligned, ldq >= n a multiple of 16;
+ *          bytes n .. ldq - 1 of a row are left as they are.
+ *   scale  [rows] fp32 out.
+ * No scratch.  Returns EXTERND_OK, EXTERND_ERR_INVALID_ARG or EXTERND_ERR_CUDA.
+ */
+int externd_quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8_t* Q,
+                          int64_t ldq, float* scale, externd_stream_t stream);
+
+/*
+ * externd_matmul_i8 -- Y = X W^T with 8-bit operands, a scale for each token
+ * and each output channel, and whole-number sums:
+ *   y_ti = scale_t wscale_i sum_j q_tj w_ij (+ bias_i)
+ * The sum is exact; it, its products with the scales and the bias are fp32,
+ * rounded once to ytype.
+ *
+ *   X       [rows][ldx] of xtype.  EXTERND_F32 / _F16 / _BF16: quantised within the call as
+ *           externd_quantize_rows does (scratch: rows * (n + 19) bytes at most, for at
+ *           most 65536 rows at a time); xscale is ignored.  EXTERND_I8:
+ *           q itself, 16-byte aligned, ldx a multiple of 16 (every row, the
+ *           last one too, holds ldx readable bytes; those past n do not
+ *           count), with xscale [rows].
+ *   W       [m][ldw] int8, 16-byte aligned, ldw >= n a multiple of 16 (as
+ *           for X).
+ *   wscale  [m] fp32; bias [m] fp32 or NULL.
+ *   rows    0 .. EXTERND_I8_MAX_ROWS; n 1 .. EXTERND_I8_MAX_INNER;
+ *           m 1 .. EXTERND_I8_MAX_OUT.
+ *   Y       [rows][ldy] of ytype (EXTERND_F32 / _F16 / _BF16) out, ldy >= m;
+ *           elements m .. ldy - 1 of a row are left as they are.
+ * Scratch is stream-ordered from the inference pool (externd_ternary_apply).
+ * Returns EXTERND_OK, EXTERND_ERR_INVALID_ARG, EXTERND_ERR_OOM or
+ * EXTERND_ERR_CUDA.
+ */
+int externd_matmul_i8(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W,
+                      int64_t ldw, const float* wscale, const float* bias, int64_t rows, int64_t n,
+                      int64_t m, void* Y, int ytype, int64_t ldy, externd_stream_t stream);
+
+/*
+ * externd_code_words -- 32-bit words of one row of `length` packed ternary
+ * codes (two bits an entry, rows padded to 128 entries); 0 when length is out
+ * of 1 .. EXTERND_I8_MAX_OUT.
+ */
+int64_t externd_code_words(int64_t length);
+
+/*
+ * externd_pack_codes -- lays the factors out once for
+ * externd_ternary_apply_i8: two-bit codes, B row by row (its components along
+ * the row), C component by component, and the bound of the component sums.
+ *   packed_B, packed_C, D, m, n, k: the factors as externd_decompose writes
+ *            them; 1 <= m <= EXTERND_I8_MAX_OUT, 1 <= n, k <=
+ *            EXTERND_I8_MAX_INNER.
+ *   codes_B  [m][externd_code_words(k)] uint32 out, 16-byte aligned.
+ *   codes_C  [k][externd_code_words(n)] uint32 out, 16-byte aligned.
+ *   bound    [1] fp32 out: max_c |D_c| sqrt(number of nonzeros of C's row c).
+ * No scratch.  Returns EXTERND_OK, EXTERND_ERR_INVALID_ARG or EXTERND_ERR_CUDA.
+ */
+int externd_pack_codes(const uint32_t* packed_B, const uint32_t* packed_C, const float* D,
+                       int64_t m, int64_t n, int64_t k, uint32_t* codes_B, uint32_t* codes_C,
+                       float* bound, externd_stream_t stream);
+
+/*
+ * externd_ternary_apply_i8 -- Y = X (B diag(D) C)^T on 8-bit activations:
+ *   T_tc = sum_j q_tj C_cj                  (whole numbers, exact)
+ *   p_tc = fl32(D_c T_tc)
+ *   z_t  = fl32(bound |q_t|_2 / 32512)      (|p_tc| <= bound |q_t|_2)
+ *   h_tc = the whole number nearest to p_tc / z_t, ties to even (0 if z_t is 0)
+ *   y_ti = scale_t (z_t sum_c B_ic h_tc)    (whole-number sum, exact)
+ * h has 16 bits and is held as two 8-bit planes, so both products are 8-bit
+ * products with whole-number sums: results do not depend on how a call is
+ * batched.  The fixed scale z_t costs log2(sqrt(n)) of h's bits against a
+ * scale from the true maximum, and saves the pass over all sums that would
+ * find it; what is left (a step of z_t) is below the step of the 8-bit
+ * activations.  fp32 arithmetic, rounded once to ytype.  A component with a
+ * NaN or infinite D makes every result NaN or 0 * infinity.
+ *
+ *   codes_B, codes_C, bound: from externd_pack_codes; D [k] the same as there.
+ *   X, xtype, ldx, xscale, rows, Y, ytype, ldy: as for externd_matmul_i8.
+ * Scratch: for each of at most 4096 rows at a time n + 2 k + 54 bytes at
+ * most, stream-ordered from the inference pool (externd_ternary_apply).
+ * Returns EXTERND_OK, EXTERND_ERR_INVALID_ARG, EXTERND_ERR_OOM or
+ * EXTERND_ERR_CUDA.
+ */
+int externd_ternary_apply_i8(const uint32_t* codes_B, const uint32_t* codes_C, const float* D,
+                             const float* bound, int64_t m, int64_t n, int64_t k, const void* X,
+                             int xtype, int64_t ldx, const float* xscale, int64_t rows, void* Y,
+                             int ytype, int64_t ldy, externd_stream_t stream);
+
+/*
  * externd_decompose_noalloc -- externd_decompose (block == 1 only) without
  * any memory allocation.  The paper has no counterpart; this is a service of
  * this library.
