@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "common.cuh"
 #include "int8.cuh"
 #include "int8_internal.h"
 #include "internal.h"
@@ -25,7 +26,7 @@ constexpr int64_t kPassRows = 4096;
 int64_t type_size(int type) { return type == EXTERND_F32 ? 4 : type == EXTERND_I8 ? 1 : 2; }
 
 int gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st) {
-  return skinny_gemm(a, epi, after_rows, st);
+  return a.rows > 32 ? mma_gemm(a, epi, after_rows, st) : skinny_gemm(a, epi, after_rows, st);
 }
 
 // Stream-ordered scratch from the library's pool, freed on the stream.
@@ -64,6 +65,7 @@ int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int
   a.ytype = ytype; a.ldy = ldy;
   a.M = (int)m; a.K = (int)n;
   a.status = status_word_ptr();
+  a.budget = kDefaultWaitBudget;
   if (!a.status) return EXTERND_ERR_CUDA;
   Scratch ws(st);
   const int64_t ldq = pad16(n);
@@ -111,6 +113,7 @@ int factors(const uint32_t* codes_B, const uint32_t* codes_C, const float* D, co
     const int64_t rr = std::min(chunk, rows - r0);
     GemmArgs a = {};
     a.status = status;
+    a.budget = kDefaultWaitBudget;
     a.rows = (int)rr;
     if (xtype == EXTERND_I8) {
       a.x = (const int8_t*)X + r0 * ldx;

@@ -17,6 +17,7 @@ int row_norms(const int8_t* Q, int64_t ldq, int64_t rows, int64_t n, const float
 int pack_codes(const uint32_t* pB, const uint32_t* pC, const float* D, int64_t m, int64_t n,
                int64_t k, uint32_t* codes_B, uint32_t* codes_C, float* rho, cudaStream_t st);
 int skinny_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
+int mma_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
 int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W, int64_t ldw,
            const float* wscale, const float* bias, int64_t rows, int64_t n, int64_t m, void* Y,
            int ytype, int64_t ldy, cudaStream_t st);
