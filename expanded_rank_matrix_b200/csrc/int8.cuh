@@ -67,38 +67,49 @@ __device__ __forceinline__ void store_out(void* y, int64_t at, int ytype, float 
     ((float*)y)[at] = v;
 }
 
-// x / s to the nearest whole number, ties to even, exactly: x * inv (inv =
-// fl(1 / s)) is within a few 2^-23 of the quotient, so its rounding q is the
-// answer or a neighbour; the remainder x - q s is a multiple of the smaller
-// operand's last place and below s, so the fused multiply-add returns it
-// without error and its comparison with s / 2 decides.  Valid for normal s
-// away from the ends of the range (safe_scale) and |x / s| < 2^16.
-__device__ __forceinline__ float nearest_quotient(float x, float s, float inv) {
-  float q = rintf(x * inv);
-  const float r = fmaf(-q, s, x);
-  const float twice = 2.f * fabsf(r);
-  if (twice > s || (twice == s && ((int)q & 1))) q += r > 0.f ? 1.f : -1.f;
-  return q;
+// x / s to the nearest whole number, ties to even, exactly, for |x / s| below
+// 2^16.  Adding 1.5 * 2^23 to x * inv (inv = fl(1 / s)) leaves the rounded
+// quotient q in the low bits of the sum (no conversion instruction, which run
+// at a quarter rate or less); it is the answer or, next to a half, a
+// neighbour.  The remainder x - q s is a multiple of the smaller operand's last
+// place and not above s, so the fused multiply-add returns it without error:
+// where it is below s / 2 in magnitude, q is right.  The others (ties among
+// them) are few and take the fp64 path, which cannot go wrong: a quotient of
+// two fp32 values does not round onto a half in fp64 without being one.
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+
+struct Rounded {
+  float shifted;    // kRound + q: its low bits are q in two's complement
+  float remainder;  // x - q s
+};
+__device__ __forceinline__ Rounded round_quotient(float x, float s, float inv) {
+  Rounded r;
+  r.shifted = fmaf(x, inv, kRound);
+  r.remainder = fmaf(kRound - r.shifted, s, x);
+  return r;
 }
+__device__ __forceinline__ uint32_t low_bits(const Rounded& r) { return __float_as_uint(r.shifted); }
+// scales for which all of that holds (away from the ends of the range)
 __device__ __forceinline__ bool safe_scale(float s) { return s > 1e-30f && s < 1e30f; }
-// the same for any s > 0 (a quotient of two fp32 values cannot round onto a
-// half in fp64 without being one)
-__device__ __forceinline__ float nearest_quotient_slow(float x, float s) {
-  return (float)rint((double)x / (double)s);
+__device__ __forceinline__ int nearest_quotient(float x, float s) {
+  return (int)rint((double)x / (double)s);
 }
 
-// Component sum -> 16-bit value (0 for z = 0 or not finite).
-__device__ __forceinline__ int component_value(float p, float z, float inv, bool safe) {
-  float q;
-  if (safe) {
-    q = nearest_quotient(p, z, inv);
-  } else {
-    if (!(z > 0.f) || isinf(z)) return 0;
-    q = nearest_quotient_slow(p, z);
-  }
-  // (|p| <= rho sqrt(r) keeps |q| <= 32512; the clamp only tames a NaN or
-  // infinite D)
-  return (int)fminf(fmaxf(q, -32512.f), 32512.f);
+// Component sum -> 16-bit value, any z (0 for z = 0 or not finite).
+__device__ __forceinline__ int component_value(float p, float z) {
+  if (!(z > 0.f) || isinf(z) || isnan(p)) return 0;
+  // (|p| <= rho |q|_2 keeps the value within 32512; the clamp only tames a D
+  // that is infinite)
+  return (int)fmin(fmax(rint((double)p / (double)z), -32512.0), 32512.0);
+}
+
+// What the epilogues keep of a token's z: {z, 1 / z, z / 2, 0}.  A column
+// whose scale is not safe gets a negative last bound, which sends its sums to
+// component_value; z = 0 (a token of zeros) gives 0 at once.
+__device__ __forceinline__ float4 component_scale(float z) {
+  if (safe_scale(z)) return make_float4(z, __fdiv_rn(1.f, z), 0.5f * z, 0.f);
+  if (z == 0.f) return make_float4(0.f, 0.f, __uint_as_float(0x7f800000u), 0.f);
+  return make_float4(z, 0.f, -1.f, 0.f);
 }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -14,15 +14,18 @@
 // The K loop runs in steps of 128 bytes through a ring of shared-memory
 // stages (128-byte swizzled rows).  Activations and 8-bit weights arrive by
 // TMA, which fills zeros past K, the last row and the last token.  Two-bit
-// codes are read by four warps, a row a thread and two 16-byte loads a step,
-// four steps ahead, unpacked in registers (two instructions for four codes)
-// and stored as the signed bytes +-64 the tensor core reads.  Accumulators
+// codes arrive by TMA too (4 KB a step) and four warps unpack them, a row a
+// thread, two instructions for four codes, into the signed bytes +-64 the
+// tensor core reads.  (With the codes loaded into the unpacking warps' own
+// registers four steps ahead, a step took about 1800 cycles: the arrival on the
+// even CTA's barrier is a release that waits for the warp's loads in flight.)  Accumulators
 // double up in tensor memory, so the epilogue of a tile runs beside the K
 // loop of the next one.
 //
 // Warp roles (per CTA): 0 TMA producer, 1 MMA issuer (even CTA of the pair),
 // 2 tensor-memory allocation, 4..7 code unpacking, 8..15 epilogue.
 // mbarriers: full (even CTA: both CTAs' copies and unpacked codes of a stage),
+// codes (each CTA: its packed codes have landed),
 // empty (each CTA: the stage's MMAs are done), accf / accfree (an accumulator
 // is complete / read out).  Every wait is bounded; one that runs out raises
 // EXTERND_ERR_TIMEOUT, and the pair winds down without further waits than
@@ -49,16 +52,18 @@ constexpr int kStages = 6;
 constexpr int kKStep = 128;                 // bytes of K per stage
 constexpr int kHalfRows = 128;              // operand rows a CTA holds, at most
 constexpr int kOperand = kHalfRows * kKStep;  // 16 KB
-constexpr int kStageBytes = 2 * kOperand;
+constexpr int kCodeRow = kKStep / 4;        // bytes of packed codes of a row and K step
+constexpr int kCodeBytes = kHalfRows * kCodeRow;  // 4 KB
+// weights, activations, packed codes (only where the weights are codes)
+constexpr int kStageBytes = 2 * kOperand + kCodeBytes;
 constexpr int kAccCols = 256;               // tensor-memory columns of an accumulator
 constexpr int kMmaThreads = 512;
 constexpr int kUnpackWarp0 = 4, kEpiWarp0 = 8, kEpiWarps = 8;
-constexpr int kAhead = 4;                   // K steps whose codes are loaded ahead
 constexpr int kMmaSmem = kStages * kStageBytes + 1024;
 static_assert(2 * kMmaSmem > 228 * 1024, "one CTA per SM: it takes all of tensor memory");
 
 struct Bars {
-  uint64_t full[kStages], empty[kStages], accf[2], accfree[2], drain;
+  uint64_t full[kStages], empty[kStages], codes[kStages], accf[2], accfree[2], drain;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -87,7 +92,7 @@ __device__ __forceinline__ void bar_expect(uint32_t a, uint32_t bytes) {
                : "memory");
 }
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t a) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
 }
 __device__ __forceinline__ bool bar_test(uint32_t a, uint32_t parity) {
   uint32_t ok;
@@ -118,6 +123,15 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const void* map, int x, int
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// into the CTA itself
+__device__ __forceinline__ void tma_2d_own(uint32_t dst, const void* map, int x, int y,
+                                           uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3}], [%4];" ::"r"(dst),
       "l"((uint64_t)map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
@@ -180,6 +194,34 @@ __device__ __forceinline__ uint32_t instr_desc(int n) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (16u << 24);
 }
 
+// 16-bit values of weight row i (a lane's own; the warp's 32 rows are
+// consecutive) and 16 tokens from t on, to the two planes.  Four lanes trade
+// bytes so that each stores four consecutive rows of one token at once.
+__device__ __forceinline__ void store_planes(const GemmArgs& a, const uint32_t (&h)[16], int i,
+                                             int t, int lane) {
+  const int i4 = i & ~3;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint32_t b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = p ? h[4 * g + e] : (h[4 * g + e] + 128u) >> 8;
+      // bytes of tokens 0..3 of this row -> rows of one token, over two exchanges
+      uint32_t w = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+      const uint32_t o1 = __shfl_xor_sync(0xffffffffu, w, 1);
+      w = (lane & 1) ? __byte_perm(w, o1, 0x3715) : __byte_perm(w, o1, 0x6240);
+      const uint32_t o2 = __shfl_xor_sync(0xffffffffu, w, 2);
+      w = (lane & 2) ? __byte_perm(w, o2, 0x3276) : __byte_perm(w, o2, 0x5410);
+      const int tt = t + 4 * g + (lane & 3);
+      if (tt < a.rows && i4 < a.M) {
+        int8_t* y = (int8_t*)a.y + (int64_t)tt * a.ldy + i4 + p * a.plane;
+        *(uint32_t*)y = w;  // (rows past M fall into the padding of the token's row)
+      }
+    }
+  }
+}
+
 // MT tiles of 256 weight rows, TT tiles of NT tokens (kOutFactors: NT / 2).
 template <bool CODES, Epilogue EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
@@ -190,7 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
   __shared__ __align__(8) Bars bars;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  __shared__ float col_s[2][kAccCols], col_inv[2][kAccCols];
+  __shared__ float4 col[2][kAccCols];  // a column's scales
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
@@ -211,6 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       bar_init(smem_u32(&bars.full[s]), CODES ? 9 : 1);
       bar_init(smem_u32(&bars.empty[s]), 1);
+      bar_init(smem_u32(&bars.codes[s]), 1);
     }
     for (int q = 0; q < 2; ++q) {
       bar_init(smem_u32(&bars.accf[q]), 1);
@@ -249,7 +292,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
           const uint32_t dst = smem_u32(ring + s * kStageBytes);
           if (rank == 0) bar_expect(bar, tx);
           const uint32_t lbar = in_leader(bar);
-          if (!CODES) tma_2d(dst, &wmap, k * kKStep, wrow, lbar);
+          if (CODES) {
+            const uint32_t cbar = smem_u32(&bars.codes[s]);
+            bar_expect(cbar, kCodeBytes);
+            tma_2d_own(dst + 2 * kOperand, &wmap, k * kCodeRow, wrow, cbar);
+          } else {
+            tma_2d(dst, &wmap, k * kKStep, wrow, lbar);
+          }
           tma_3d(dst + kOperand, &xmap, k * kKStep, trow, plane, lbar);
         }
         if (!ok) break;
@@ -292,59 +341,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
     // ---- codes: a row a thread ----
     const int row = (wid - kUnpackWarp0) * 32 + lane;
     const uint32_t sw = (uint32_t)(row & 7);
-    const int groups = (ksteps + kAhead - 1) / kAhead;
-    const uint4* src = nullptr;
-    uint4 next[2 * kAhead];
-    auto fetch = [&](int tile, int g) {
-      if (g == 0) {
-        const int wi = min((tile % MT) * 256 + rank * kHalfRows + row, a.M - 1);
-        src = (const uint4*)((const uint32_t*)a.w + (int64_t)wi * a.ldw);
+    const int mine = pair < tiles ? (tiles - pair + npairs - 1) / npairs * ksteps : 0;
+    for (int i = 0; i < mine; ++i) {
+      const int s = i % kStages;
+      const bool got = bar_wait(smem_u32(&bars.codes[s]), (i / kStages) & 1, ab, a.budget);
+      if (!__all_sync(0xffffffffu, got)) break;
+      unsigned char* stage = ring + s * kStageBytes;
+      // (the two halves of a row are read in an order that keeps the lanes of
+      // a quarter warp on distinct banks)
+      uint4 c[2];
+      const uint4* src = (const uint4*)(stage + 2 * kOperand + row * kCodeRow);
+      const int first = (row >> 2) & 1;
+      c[0] = src[first];
+      c[1] = src[first ^ 1];
+      if (first) {
+        const uint4 u = c[0];
+        c[0] = c[1];
+        c[1] = u;
       }
+      unsigned char* dst = stage + row * kKStep;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int k = g * kAhead + u;
-        if (k < ksteps) {
-          next[2 * u] = __ldg(src + 2 * k);
-          next[2 * u + 1] = __ldg(src + 2 * k + 1);
-        }
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t w = ((const uint32_t*)c)[j];
+        *(uint4*)(dst + (((uint32_t)j ^ sw) << 4)) = make_uint4(
+            w & kCodeMask, (w << 2) & kCodeMask, (w << 4) & kCodeMask, (w << 6) & kCodeMask);
       }
-    };
-    int i = 0;
-    bool ok = true;
-    if (pair < tiles) fetch(pair, 0);
-    for (int tile = pair; tile < tiles && ok; tile += npairs) {
-      for (int g = 0; g < groups && ok; ++g) {
-        uint4 cur[2 * kAhead];
-#pragma unroll
-        for (int u = 0; u < 2 * kAhead; ++u) cur[u] = next[u];
-        if (g + 1 < groups)
-          fetch(tile, g + 1);
-        else if (tile + npairs < tiles)
-          fetch(tile + npairs, 0);
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (g * kAhead + u < ksteps && ok) {
-            const int s = i % kStages;
-            bool got = i < kStages ||
-                       bar_wait(smem_u32(&bars.empty[s]), ((i / kStages) + 1) & 1, ab, a.budget);
-            ok = __all_sync(0xffffffffu, got);
-            if (ok) {
-              unsigned char* dst = ring + s * kStageBytes + row * kKStep;
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const uint32_t w = ((const uint32_t*)&cur[2 * u])[c];
-                *(uint4*)(dst + (((uint32_t)c ^ sw) << 4)) =
-                    make_uint4(w & kCodeMask, (w << 2) & kCodeMask, (w << 4) & kCodeMask,
-                               (w << 6) & kCodeMask);
-              }
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
-              if (lane == 0) bar_arrive_cluster(in_leader(smem_u32(&bars.full[s])));
-              ++i;
-            }
-          }
-        }
-      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive_cluster(in_leader(smem_u32(&bars.full[s])));
     }
   } else if (wid >= kEpiWarp0) {
     // ---- epilogue: warp w reads lanes 32 (w % 4) .., one half of the columns ----
@@ -360,18 +384,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
       // the tile between)
       if (et < per) {
         const int t = t0 + et;
-        float s = 0.f, v = 0.f;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         if (t < a.rows) {
-          if (EPI == kOutPlanes) {
-            s = a.z[t];
-            v = safe_scale(s) ? __fdiv_rn(1.f, s) : 0.f;
-          } else {
-            s = a.xscale[t];
-            if (EPI == kOutFactors) v = a.z[t];
-          }
+          if (EPI == kOutPlanes)
+            s = component_scale(a.z[t]);
+          else
+            s.x = a.xscale[t], s.y = EPI == kOutFactors ? a.z[t] : 0.f;
         }
-        col_s[q][et] = s;
-        col_inv[q][et] = v;
+        col[q][et] = s;
       }
       const float ws = EPI != kOutFactors && i < a.M ? a.wscale[i] : 0.f;
       const float bias = EPI == kOutDense && a.bias && i < a.M ? a.bias[i] : 0.f;
@@ -387,28 +407,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
           acc_load(acc + c0, v);
           if (EPI == kOutFactors) acc_load(acc + half + c0, lo);
           acc_wait();
-          if (i < a.M) {
+          if (EPI == kOutPlanes) {
+            uint32_t h[16];
+            bool far = false;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float4 s = col[q][c0 + e];
+              const Rounded r = round_quotient(ws * (float)(v[e] >> kCodeShift), s.x, s.y);
+              h[e] = low_bits(r);
+              far = far || !(fabsf(r.remainder) < s.z);
+            }
+            if (far) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                h[e] = (uint32_t)component_value(ws * (float)(v[e] >> kCodeShift), col[q][c0 + e].x);
+            }
+            store_planes(a, h, i, t0 + c0, lane);
+          } else if (i < a.M) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const int t = t0 + c0 + e;
               if (t >= a.rows) break;
-              const float s = col_s[q][c0 + e];
+              const float4 s = col[q][c0 + e];
+              float y;
               if (EPI == kOutDense) {
                 const float p = ws * (float)v[e];
-                const float y = a.bias ? fmaf(s, p, bias) : s * p;
-                store_out(a.y, (int64_t)t * a.ldy + i, a.ytype, y);
-              } else if (EPI == kOutPlanes) {
-                const float inv = col_inv[q][c0 + e];
-                const int h =
-                    component_value(ws * (float)(v[e] >> kCodeShift), s, inv, inv != 0.f);
-                const int hi = (h + 128) >> 8;
-                int8_t* y = (int8_t*)a.y + (int64_t)t * a.ldy + i;
-                y[0] = (int8_t)hi;
-                y[a.plane] = (int8_t)(h - 256 * hi);
+                y = a.bias ? fmaf(s.x, p, bias) : s.x * p;
               } else {
-                const float sum = fmaf(256.f, (float)(v[e] >> kCodeShift), (float)(lo[e] >> kCodeShift));
-                store_out(a.y, (int64_t)t * a.ldy + i, a.ytype, s * (col_inv[q][c0 + e] * sum));
+                y = s.x * (s.y * fmaf(256.f, (float)(v[e] >> kCodeShift), (float)(lo[e] >> kCodeShift)));
               }
+              store_out(a.y, (int64_t)t * a.ldy + i, a.ytype, y);
             }
           }
         }
@@ -450,18 +478,19 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// Byte rows [planes][rows][ld], K of them read; boxes of 128 bytes x `box`
-// rows, 128-byte swizzle, zeros outside.
-bool byte_map(CUtensorMap* tm, const void* p, int K, int rows, int64_t ld, int planes,
-              int64_t plane, int box, bool three) {
+// Byte rows [planes][rows][ld], `bytes` of them read; boxes of `inner` bytes x
+// `box` rows, zeros outside.
+bool byte_map(CUtensorMap* tm, const void* p, int64_t bytes, int rows, int64_t ld, int planes,
+              int64_t plane, int inner, int box) {
   const auto fn = tensor_map_encoder();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, (cuuint64_t)planes};
+  const cuuint64_t dims[3] = {(cuuint64_t)bytes, (cuuint64_t)rows, (cuuint64_t)planes};
   const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)plane};
-  const cuuint32_t boxes[3] = {(cuuint32_t)kKStep, (cuuint32_t)box, 1};
+  const cuuint32_t boxes[3] = {(cuuint32_t)inner, (cuuint32_t)box, 1};
   const cuuint32_t step[3] = {1, 1, 1};
-  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, three ? 3 : 2, (void*)p, dims, strides, boxes, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, planes ? 3 : 2, (void*)p, dims, strides, boxes, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            inner == kKStep ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -498,11 +527,9 @@ int launch(const GemmArgs& a, bool after_rows, cudaStream_t st) {
   const long long TT = ((long long)a.rows * P + NT - 1) / NT;
   if (MT * TT > 2147483647LL) return EXTERND_ERR_INVALID_ARG;
   CUtensorMap xmap, wmap;
-  if (!byte_map(&xmap, a.x, a.K, a.rows, a.ldx, P, P == 2 ? a.plane : a.ldx, NT / 2, true))
-    return EXTERND_ERR_CUDA;
-  if (CODES)
-    wmap = xmap;
-  else if (!byte_map(&wmap, a.w, a.K, a.M, a.ldw, 1, 0, kHalfRows, false))
+  if (!byte_map(&xmap, a.x, a.K, a.rows, a.ldx, P, P == 2 ? a.plane : a.ldx, kKStep, NT / 2) ||
+      !(CODES ? byte_map(&wmap, a.w, 4 * a.ldw, a.M, 4 * a.ldw, 0, 0, kCodeRow, kHalfRows)
+              : byte_map(&wmap, a.w, a.K, a.M, a.ldw, 0, 0, kKStep, kHalfRows)))
     return EXTERND_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)std::min<long long>(pairs, MT * TT));

@@ -8,6 +8,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "common.cuh"
@@ -18,8 +19,6 @@
 namespace externd {
 namespace i8 {
 namespace {
-
-constexpr int kHeld = 8;  // 16-byte vectors of its row that a thread holds
 
 template <typename T>
 struct RowArgs {
@@ -35,115 +34,151 @@ struct RowArgs {
   int* status;
 };
 
-// E elements at x[j ..] (zeros past n); VEC: every row starts 16-byte aligned
+// Where a thread's vector h lies in the row, and the distance of its elements:
+// aligned rows are read in 16-byte vectors, others an element at a time with
+// neighbouring threads on neighbouring elements.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_vec(const T* x, int j, int n, T (&v)[16 / sizeof(T)]) {
+__device__ __forceinline__ int first_of(int h, int tid, int G) {
+  constexpr int E = 16 / sizeof(T);
+  return VEC ? (h * G + tid) * E : h * G * E + tid;
+}
+
+// E elements from j on (zeros past n)
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_vec(const T* x, int j, int n, int G, T (&v)[16 / sizeof(T)]) {
   constexpr int E = 16 / sizeof(T);
   if (VEC && j + E <= n) {
     *(uint4*)v = __ldg((const uint4*)(x + j));
   } else {
+    const int step = VEC ? 1 : G;
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = j + e < n ? x[j + e] : T(0.f);
+    for (int e = 0; e < E; ++e) v[e] = j + e * step < n ? x[j + e * step] : T(0.f);
   }
 }
 
-// Sum or maximum over the G threads of a row group; every thread gets it.
-template <int G, bool MAX>
+// Largest magnitude bits seen so far: the bit patterns of non-negative floats
+// order like integers in every type, and a NaN is above infinity.
+__device__ __forceinline__ uint32_t top_bits(uint32_t top, const float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+  return top;
+}
+template <typename T>  // 16-bit types: two magnitudes side by side
+__device__ __forceinline__ uint32_t top_bits(uint32_t top, const T (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = __vmaxu2(top, ((const uint32_t*)v)[e] & 0x7fff7fffu);
+  return top;
+}
+// the magnitude those bits stand for (as fp32 bits)
+__device__ __forceinline__ uint32_t top_value(uint32_t top, float) { return top; }
+template <typename T>
+__device__ __forceinline__ uint32_t top_value(uint32_t top, T) {
+  const uint16_t u = (uint16_t)max(top & 0xffffu, top >> 16);
+  T h;
+  *(uint16_t*)&h = u;
+  return __float_as_uint(to_f32(h)) & 0x7fffffffu;
+}
+
+// Sum or maximum over a warp, or over the CTA; every thread gets it.  `red`
+// is used once in a launch.
+template <bool WARP, bool MAX>
 __device__ __forceinline__ uint32_t group_reduce(uint32_t v, uint32_t* red) {
   v = MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_add_sync(0xffffffffu, v);
-  if (G == 32) return v;
-  constexpr int W = G / 32;
+  if (WARP) return v;
   const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __syncthreads();
   if (lane == 0) red[wid] = v;
   __syncthreads();
-  v = lane < W ? red[(wid / W) * W + lane] : 0u;
+  v = lane < (int)(blockDim.x >> 5) ? red[lane] : 0u;
   return MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_add_sync(0xffffffffu, v);
 }
 
-// G threads a row; blockDim.x / G rows a CTA.
-template <typename T, int G, bool VEC>
-__global__ void __launch_bounds__(G > 256 ? G : 256) rows_kernel(const RowArgs<T> a) {
+constexpr int kWarpRows = 8;  // rows of a CTA where a warp takes a row
+
+// A warp (WARP) or a CTA takes a row; a thread holds H 16-byte vectors of it.
+template <typename T, int H, bool VEC, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rows_kernel(const RowArgs<T> a) {
   constexpr int E = 16 / sizeof(T);
-  __shared__ uint32_t red[32];
+  __shared__ uint32_t red[2][32];
   pdl_trigger();
-  const int tid = threadIdx.x % G;
-  const int64_t row0 = (int64_t)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
-  const bool live = row0 < a.rows;
-  const int64_t row = live ? row0 : a.rows - 1;  // (whole warps take part in the reductions)
+  const int G = WARP ? 32 : (int)blockDim.x;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t row = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  if (row >= a.rows) return;  // (whole warps; never in a CTA with a row)
   const T* x = a.x + row * a.ldx;
-  T v[kHeld][E];
-  // magnitudes as the bit patterns of non-negative floats, which order like
-  // integers; a NaN is above infinity, so one comparison finds either
+  T v[H][E];
   uint32_t top = 0u;
 #pragma unroll
-  for (int h = 0; h < kHeld; ++h) {
-    const int j = (h * G + tid) * E;
-    if (j < a.n) {
-      load_vec<T, VEC>(x, j, a.n, v[h]);
-#pragma unroll
-      for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(to_f32(v[h][e])) & 0x7fffffffu);
-    }
+  for (int h = 0; h < H; ++h) {
+    const int j = first_of<T, VEC>(h, tid, G);
+    if (j < a.n) load_vec<T, VEC>(x, j, a.n, G, v[h]);
   }
-  for (int j = (kHeld * G + tid) * E; j < a.n; j += G * E) {
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    if (first_of<T, VEC>(h, tid, G) < a.n) top = top_bits(top, v[h]);
+  for (int h = H; first_of<T, VEC>(h, 0, G) < a.n; ++h) {
     T u[E];
-    load_vec<T, VEC>(x, j, a.n, u);
-#pragma unroll
-    for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(to_f32(u[e])) & 0x7fffffffu);
+    load_vec<T, VEC>(x, first_of<T, VEC>(h, tid, G), a.n, G, u);
+    top = top_bits(top, u);
   }
-  top = group_reduce<G, true>(top, red);
+  top = group_reduce<WARP, true>(top_value(top, T(0.f)), red[0]);
   const bool finite = top < 0x7f800000u;
   const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.f) : __uint_as_float(0x7fc00000u);
   const bool safe = safe_scale(s);
-  const float inv = safe ? __fdiv_rn(1.f, s) : 0.f;
-  if (live && tid == 0) {
+  const float inv = safe ? __fdiv_rn(1.f, s) : 0.f, half = 0.5f * s;
+  if (tid == 0) {
     a.scale[row] = s;
     if (!finite) atomicCAS(a.status, 0, EXTERND_ERR_NONFINITE);
   }
   int8_t* q = a.q + row * a.ldq;
   uint32_t squares = 0u;
   auto emit = [&](int j, const T (&u)[E]) {
+    uint32_t b[E];
+    float far = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const Rounded r = round_quotient(to_f32(u[e]), s, inv);
+      b[e] = low_bits(r);
+      far = fmaxf(far, fabsf(r.remainder));
+    }
+    if (!(far < half) || !safe) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        // (a subnormal scale may put x / s past 127: the clamp keeps 8 bits)
+        b[e] = s > 0.f ? (uint32_t)max(-127, min(127, nearest_quotient(to_f32(u[e]), s))) : 0u;
+    }
     uint32_t packed[E / 4];
 #pragma unroll
     for (int p = 0; p < E / 4; ++p) {
-      uint32_t word = 0u;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float f = to_f32(u[4 * p + e]);
-        // (a subnormal scale may put x / s past 127: the clamp keeps 8 bits)
-        const float r = safe ? nearest_quotient(f, s, inv)
-                        : s > 0.f ? fminf(fmaxf(nearest_quotient_slow(f, s), -127.f), 127.f)
-                                  : 0.f;
-        word |= ((uint32_t)(int)r & 0xffu) << (8 * e);
-      }
-      packed[p] = word;
-      squares = __dp4a((int)word, (int)word, (int)squares);
+      packed[p] = __byte_perm(__byte_perm(b[4 * p], b[4 * p + 1], 0x0040),
+                              __byte_perm(b[4 * p + 2], b[4 * p + 3], 0x0040), 0x5410);
+      squares = __dp4a((int)packed[p], (int)packed[p], (int)squares);
     }
-    if (!live) return;
-    if (j + E <= a.n) {
+    if (VEC && j + E <= a.n) {
       if (E == 8)
         *(uint2*)(q + j) = make_uint2(packed[0], packed[E / 4 - 1]);
       else
         *(uint32_t*)(q + j) = packed[0];
     } else {
+      const int step = VEC ? 1 : G;
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (j + e < a.n) q[j + e] = (int8_t)(packed[e / 4] >> (8 * (e & 3)));
+        if (j + e * step < a.n) q[j + e * step] = (int8_t)b[e];
     }
   };
 #pragma unroll
-  for (int h = 0; h < kHeld; ++h) {
-    const int j = (h * G + tid) * E;
+  for (int h = 0; h < H; ++h) {
+    const int j = first_of<T, VEC>(h, tid, G);
     if (j < a.n) emit(j, v[h]);
   }
-  for (int j = (kHeld * G + tid) * E; j < a.n; j += G * E) {
+  for (int h = H; first_of<T, VEC>(h, 0, G) < a.n; ++h) {
+    const int j = first_of<T, VEC>(h, tid, G);
     T u[E];
-    load_vec<T, VEC>(x, j, a.n, u);
+    load_vec<T, VEC>(x, j, a.n, G, u);
     emit(j, u);
   }
   if (a.z) {
-    squares = group_reduce<G, false>(squares, red);
-    if (live && tid == 0)
+    squares = group_reduce<WARP, false>(squares, red[1]);
+    if (tid == 0)
       a.z[row] = (float)((double)__ldg(a.rho) * sqrt((double)squares) / kFullScale);
   }
 }
@@ -174,24 +209,32 @@ __global__ void __launch_bounds__(256) row_norm_kernel(const int8_t* __restrict_
   if (lane == 0) z[row] = (float)((double)__ldg(rho) * sqrt((double)total) / kFullScale);
 }
 
-template <typename T, int G, bool VEC>
-int launch_rows_g(const RowArgs<T>& a, cudaStream_t st) {
-  constexpr int threads = G > 256 ? G : 256;
-  constexpr int per = threads / G;
-  const int64_t grid = (a.rows + per - 1) / per;
-  if (grid > 2147483647LL) return EXTERND_ERR_INVALID_ARG;
-  rows_kernel<T, G, VEC><<<(unsigned)grid, threads, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return EXTERND_ERR_CUDA;
-  return EXTERND_OK;
+template <typename T, int H, bool WARP>
+int launch_rows_h(const RowArgs<T>& a, int threads, cudaStream_t st) {
+  const bool vec = ((uintptr_t)a.x & 15) == 0 && (a.ldx * (int64_t)sizeof(T)) % 16 == 0;
+  const int64_t grid = WARP ? (a.rows + kWarpRows - 1) / kWarpRows : a.rows;
+  if (vec)
+    rows_kernel<T, H, true, WARP><<<(unsigned)grid, threads, 0, st>>>(a);
+  else
+    rows_kernel<T, H, false, WARP><<<(unsigned)grid, threads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? EXTERND_OK : EXTERND_ERR_CUDA;
 }
 
+// HBM stays busy through the bytes in flight on an SM and many small CTAs
+// whose load, reduction and store phases overlap.  Five vectors a thread were
+// best wherever there are rows enough (8192 x 9728 bf16: 51 us, against 178,
+// 109, 71, 58, 54 and 65 us with 1, 2, 3, 4, 6 and 8; 2048 x 9728 fp32: 24 us
+// against 25 .. 50); a few rows take two, as the time of one row counts.
 template <typename T>
 int launch_rows(const RowArgs<T>& a, cudaStream_t st) {
-  const bool vec = ((uintptr_t)a.x & 15) == 0 && (a.ldx * (int64_t)sizeof(T)) % 16 == 0;
-  // a warp holds 4 KB of a row: longer rows take a CTA each
-  const bool wide = a.n * (int64_t)sizeof(T) > 32 * kHeld * 16;
-  if (wide) return vec ? launch_rows_g<T, 256, true>(a, st) : launch_rows_g<T, 256, false>(a, st);
-  return vec ? launch_rows_g<T, 32, true>(a, st) : launch_rows_g<T, 32, false>(a, st);
+  const int vecs = (int)((a.n * (int64_t)sizeof(T) + 15) / 16);
+  auto threads = [&](int held) { return std::min(((vecs + held - 1) / held + 31) / 32 * 32, 1024); };
+  if (a.rows <= 256) {
+    if (vecs <= 32 * 2) return launch_rows_h<T, 2, true>(a, 32 * kWarpRows, st);
+    if (vecs <= 1024 * 2) return launch_rows_h<T, 2, false>(a, threads(2), st);
+  }
+  if (vecs <= 32 * 5) return launch_rows_h<T, 5, true>(a, 32 * kWarpRows, st);
+  return launch_rows_h<T, 5, false>(a, threads(5), st);
 }
 
 template <typename T>

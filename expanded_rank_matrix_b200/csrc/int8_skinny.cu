@@ -152,9 +152,7 @@ __global__ void __launch_bounds__(kSkThreads) skinny_kernel(const GemmArgs a) {
       if (a.bias) v = fmaf(a.xscale[t], a.wscale[i] * (float)s[0], a.bias[i]);
       store_out(a.y, (int64_t)t * a.ldy + i, a.ytype, v);
     } else if (EPI == kOutPlanes) {
-      const float z = a.z[t];
-      const bool safe = safe_scale(z);
-      const int h = component_value(a.wscale[i] * (float)s[0], z, safe ? __fdiv_rn(1.f, z) : 0.f, safe);
+      const int h = component_value(a.wscale[i] * (float)s[0], a.z[t]);
       const int hi = (h + 128) >> 8;
       int8_t* y = (int8_t*)a.y + (int64_t)t * a.ldy + i;
       y[0] = (int8_t)hi;
