@@ -74,6 +74,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// One lane of a whole warp.  The issuing loops run under this and not under
+// lane == 0: the operands of the tensor-core and copy instructions are
+// warp-uniform registers, and only here the compiler knows one lane to be
+// active (a K step's four MMAs took 494 cycles to issue otherwise).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(one));
+  return one != 0u;
+}
 // the same shared-memory address in the even CTA of the pair
 __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
   uint32_t r;
@@ -272,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
   pdl_wait();
 
   if (wid == 0) {
-    if (lane == 0) {  // ---- TMA producer ----
+    if (elect_one()) {  // ---- TMA producer ----
       const uint32_t tx = 2u * (uint32_t)((CODES ? 0 : kOperand) + half * kKStep);
       int i = 0;
       for (int tile = pair; tile < tiles; tile += npairs) {
@@ -305,7 +315,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
       }
     }
   } else if (wid == 1) {
-    if (rank == 0 && lane == 0) {  // ---- MMA issuer ----
+    const bool one = elect_one();
+    if (rank == 0 && one) {  // ---- MMA issuer ----
       const uint32_t idesc = instr_desc(NT);
       int i = 0, seg = 0;
       bool ok = true;
@@ -333,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
       mma_commit(smem_u32(&bars.drain));
     }
     // both CTAs stay until every MMA is done and its arrivals have come
-    if (lane == 0) {
+    if (one) {
       int never = 0;
       bar_wait(smem_u32(&bars.drain), 0u, &never, kDefaultWaitBudget);
     }
