@@ -72,10 +72,8 @@ __device__ __forceinline__ void store_out(void* y, int64_t at, int ytype, float 
 // quotient q in the low bits of the sum (no conversion instruction, which run
 // at a quarter rate or less); it is the answer or, next to a half, a
 // neighbour.  The remainder x - q s is a multiple of the smaller operand's last
-// place and not above s, so the fused multiply-add returns it without error:
-// where it is below s / 2 in magnitude, q is right.  The others (ties among
-// them) are few and take the fp64 path, which cannot go wrong: a quotient of
-// two fp32 values does not round onto a half in fp64 without being one.
+// place and not above s, so the fused multiply-add returns it without error,
+// and its comparison with s / 2 settles the answer.
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23
 
 struct Rounded {
@@ -89,8 +87,17 @@ __device__ __forceinline__ Rounded round_quotient(float x, float s, float inv) {
   return r;
 }
 __device__ __forceinline__ uint32_t low_bits(const Rounded& r) { return __float_as_uint(r.shifted); }
+// the low bits of the answer; half = s / 2
+__device__ __forceinline__ uint32_t settled(const Rounded& r, float half) {
+  const uint32_t q = low_bits(r);
+  const float far = fabsf(r.remainder);
+  if (far > half || (far == half && (q & 1u))) return r.remainder > 0.f ? q + 1u : q - 1u;
+  return q;
+}
 // scales for which all of that holds (away from the ends of the range)
 __device__ __forceinline__ bool safe_scale(float s) { return s > 1e-30f && s < 1e30f; }
+// any s > 0: a quotient of two fp32 values does not round onto a half in fp64
+// without being one
 __device__ __forceinline__ int nearest_quotient(float x, float s) {
   return (int)rint((double)x / (double)s);
 }

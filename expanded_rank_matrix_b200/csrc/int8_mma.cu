@@ -14,7 +14,7 @@
 // The K loop runs in steps of 128 bytes through a ring of shared-memory
 // stages (128-byte swizzled rows).  Activations and 8-bit weights arrive by
 // TMA, which fills zeros past K, the last row and the last token.  Two-bit
-// codes arrive by TMA too (4 KB a step) and four warps unpack them, a row a
+// codes arrive by TMA too (4 KB a step) and two groups of four warps unpack them, a row a
 // thread, two instructions for four codes, into the signed bytes +-64 the
 // tensor core reads.  (With the codes loaded into the unpacking warps' own
 // registers four steps ahead, a step took about 1800 cycles: the arrival on the
@@ -23,7 +23,8 @@
 // loop of the next one.
 //
 // Warp roles (per CTA): 0 TMA producer, 1 MMA issuer (even CTA of the pair),
-// 2 tensor-memory allocation, 4..7 code unpacking, 8..15 epilogue.
+// 2 tensor-memory allocation, then (codes only) two groups of four that unpack
+// alternate steps, and eight for the epilogue.
 // mbarriers: full (even CTA: both CTAs' copies and unpacked codes of a stage),
 // codes (each CTA: its packed codes have landed),
 // empty (each CTA: the stage's MMAs are done), accf / accfree (an accumulator
@@ -57,9 +58,13 @@ constexpr int kCodeBytes = kHalfRows * kCodeRow;  // 4 KB
 // weights, activations, packed codes (only where the weights are codes)
 constexpr int kStageBytes = 2 * kOperand + kCodeBytes;
 constexpr int kAccCols = 256;               // tensor-memory columns of an accumulator
-constexpr int kMmaThreads = 512;
-constexpr int kUnpackWarp0 = 4, kEpiWarp0 = 8, kEpiWarps = 8;
+constexpr int kUnpackWarp0 = 4, kUnpackGroups = 2, kEpiWarps = 8;
+constexpr int epi_warp0(bool codes) { return kUnpackWarp0 + (codes ? 4 * kUnpackGroups : 0); }
+constexpr int mma_threads(bool codes) { return 32 * (epi_warp0(codes) + kEpiWarps); }
 constexpr int kMmaSmem = kStages * kStageBytes + 1024;
+// a group waits on a stage's barrier by phase parity: it has to have seen the
+// stage's previous fill
+static_assert(kStages % kUnpackGroups == 0, "unpacking groups own whole stages");
 static_assert(2 * kMmaSmem > 228 * 1024, "one CTA per SM: it takes all of tensor memory");
 
 struct Bars {
@@ -204,6 +209,25 @@ __device__ __forceinline__ uint32_t instr_desc(int n) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (16u << 24);
 }
 
+__device__ __forceinline__ void round_to(float v, float& y) { y = v; }
+__device__ __forceinline__ void round_to(float v, __half& y) { y = __float2half_rn(v); }
+__device__ __forceinline__ void round_to(float v, __nv_bfloat16& y) { y = __float2bfloat16_rn(v); }
+
+// Results of one weight row for up to 16 tokens (`left` of them exist).  A
+// whole group goes without a check for each, so that its loads, arithmetic
+// and stores overlap.
+template <typename T>
+__device__ __forceinline__ void store_column(T* y, int64_t ldy, int left, const float (&v)[16]) {
+  if (left >= 16) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) round_to(v[e], y[e * ldy]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (e < left) round_to(v[e], y[e * ldy]);
+  }
+}
+
 // 16-bit values of weight row i (a lane's own; the warp's 32 rows are
 // consecutive) and 16 tokens from t on, to the two planes.  Four lanes trade
 // bytes so that each stores four consecutive rows of one token at once.
@@ -234,7 +258,7 @@ __device__ __forceinline__ void store_planes(const GemmArgs& a, const uint32_t (
 
 // MT tiles of 256 weight rows, TT tiles of NT tokens (kOutFactors: NT / 2).
 template <bool CODES, Epilogue EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 1)
     mma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                const GemmArgs a, int NT, int MT, int TT) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -243,6 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ float4 col[2][kAccCols];  // a column's scales
+  constexpr int kEpiWarp0 = epi_warp0(CODES);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
@@ -348,12 +373,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
       int never = 0;
       bar_wait(smem_u32(&bars.drain), 0u, &never, kDefaultWaitBudget);
     }
-  } else if (CODES && wid >= kUnpackWarp0 && wid < kUnpackWarp0 + 4) {
-    // ---- codes: a row a thread ----
-    const int row = (wid - kUnpackWarp0) * 32 + lane;
+  } else if (CODES && wid >= kUnpackWarp0 && wid < kEpiWarp0) {
+    // ---- codes: a row a thread, the groups of four warps on alternate steps ----
+    const int row = (wid & 3) * 32 + lane;
     const uint32_t sw = (uint32_t)(row & 7);
     const int mine = pair < tiles ? (tiles - pair + npairs - 1) / npairs * ksteps : 0;
-    for (int i = 0; i < mine; ++i) {
+    for (int i = (wid - kUnpackWarp0) >> 2; i < mine; i += kUnpackGroups) {
       const int s = i % kStages;
       const bool got = bar_wait(smem_u32(&bars.codes[s]), (i / kStages) & 1, ab, a.budget);
       if (!__all_sync(0xffffffffu, got)) break;
@@ -420,35 +445,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
           acc_wait();
           if (EPI == kOutPlanes) {
             uint32_t h[16];
-            bool far = false;
+            bool odd = false;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float4 s = col[q][c0 + e];
-              const Rounded r = round_quotient(ws * (float)(v[e] >> kCodeShift), s.x, s.y);
-              h[e] = low_bits(r);
-              far = far || !(fabsf(r.remainder) < s.z);
+              const float p = ws * (float)(v[e] >> kCodeShift);
+              const Rounded r = round_quotient(p, s.x, s.y);
+              h[e] = settled(r, s.z);
+              odd = odd || s.z < 0.f;
             }
-            if (far) {
+            if (odd) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                h[e] = (uint32_t)component_value(ws * (float)(v[e] >> kCodeShift), col[q][c0 + e].x);
+              for (int e = 0; e < 16; ++e) {
+                const float4 s = col[q][c0 + e];
+                if (s.z < 0.f)
+                  h[e] = (uint32_t)component_value(ws * (float)(v[e] >> kCodeShift), s.x);
+              }
             }
             store_planes(a, h, i, t0 + c0, lane);
-          } else if (i < a.M) {
+          } else {
+            float y[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int t = t0 + c0 + e;
-              if (t >= a.rows) break;
               const float4 s = col[q][c0 + e];
-              float y;
               if (EPI == kOutDense) {
                 const float p = ws * (float)v[e];
-                y = a.bias ? fmaf(s.x, p, bias) : s.x * p;
+                y[e] = a.bias ? fmaf(s.x, p, bias) : s.x * p;
               } else {
-                y = s.x * (s.y * fmaf(256.f, (float)(v[e] >> kCodeShift), (float)(lo[e] >> kCodeShift)));
+                y[e] = s.x *
+                       (s.y * fmaf(256.f, (float)(v[e] >> kCodeShift), (float)(lo[e] >> kCodeShift)));
               }
-              store_out(a.y, (int64_t)t * a.ldy + i, a.ytype, y);
             }
+            const int64_t at = (int64_t)(t0 + c0) * a.ldy + i;
+            const int left = i < a.M ? a.rows - (t0 + c0) : 0;
+            if (a.ytype == EXTERND_BF16)
+              store_column((__nv_bfloat16*)a.y + at, a.ldy, left, y);
+            else if (a.ytype == EXTERND_F16)
+              store_column((__half*)a.y + at, a.ldy, left, y);
+            else
+              store_column((float*)a.y + at, a.ldy, left, y);
           }
         }
       }
@@ -544,7 +579,7 @@ int launch(const GemmArgs& a, bool after_rows, cudaStream_t st) {
     return EXTERND_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)std::min<long long>(pairs, MT * TT));
-  cfg.blockDim = dim3(kMmaThreads);
+  cfg.blockDim = dim3(mma_threads(CODES));
   cfg.dynamicSmemBytes = kMmaSmem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];

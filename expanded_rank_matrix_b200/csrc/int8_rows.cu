@@ -133,18 +133,22 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rows_kernel(cons
   uint32_t squares = 0u;
   auto emit = [&](int j, const T (&u)[E]) {
     uint32_t b[E];
+    Rounded r[E];
     float far = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const Rounded r = round_quotient(to_f32(u[e]), s, inv);
-      b[e] = low_bits(r);
-      far = fmaxf(far, fabsf(r.remainder));
+      r[e] = round_quotient(to_f32(u[e]), s, inv);
+      b[e] = low_bits(r[e]);
+      far = fmaxf(far, fabsf(r[e].remainder));
     }
-    if (!(far < half) || !safe) {
+    if (!safe) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
         // (a subnormal scale may put x / s past 127: the clamp keeps 8 bits)
         b[e] = s > 0.f ? (uint32_t)max(-127, min(127, nearest_quotient(to_f32(u[e]), s))) : 0u;
+    } else if (far >= half) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) b[e] = settled(r[e], half);
     }
     uint32_t packed[E / 4];
 #pragma unroll
