@@ -110,14 +110,10 @@ __device__ __forceinline__ int component_value(float p, float z) {
   return (int)fmin(fmax(rint((double)p / (double)z), -32512.0), 32512.0);
 }
 
-// What the epilogues keep of a token's z: {z, 1 / z, z / 2, 0}.  A column
-// whose scale is not safe gets a negative last bound, which sends its sums to
-// component_value; z = 0 (a token of zeros) gives 0 at once.
-__device__ __forceinline__ float4 component_scale(float z) {
-  if (safe_scale(z)) return make_float4(z, __fdiv_rn(1.f, z), 0.5f * z, 0.f);
-  if (z == 0.f) return make_float4(0.f, 0.f, __uint_as_float(0x7f800000u), 0.f);
-  return make_float4(z, 0.f, -1.f, 0.f);
-}
+// Scales z for which an epilogue may divide by fp32 arithmetic.  The lower end
+// also covers D / 64, which the tensor-core epilogue uses in place of D: where
+// that is inexact (|D| < 2^-120), |p| < 2^-96 is less than half of such a z.
+__device__ __forceinline__ bool safe_component_scale(float z) { return z > 1e-26f && z < 1e30f; }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {

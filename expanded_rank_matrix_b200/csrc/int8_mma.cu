@@ -189,6 +189,17 @@ __device__ __forceinline__ void acc_load(uint32_t taddr, int (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+// barrier of the epilogue warps; whether any thread brought true
+__device__ __forceinline__ bool bar_any(bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 256, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(any)
+      : "r"((uint32_t)v)
+      : "memory");
+  return any != 0u;
+}
 __device__ __forceinline__ void acc_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -228,31 +239,89 @@ __device__ __forceinline__ void store_column(T* y, int64_t ldy, int left, const 
   }
 }
 
-// 16-bit values of weight row i (a lane's own; the warp's 32 rows are
-// consecutive) and 16 tokens from t on, to the two planes.  Four lanes trade
-// bytes so that each stores four consecutive rows of one token at once.
-__device__ __forceinline__ void store_planes(const GemmArgs& a, const uint32_t (&h)[16], int i,
-                                             int t, int lane) {
-  const int i4 = i & ~3;
+// Two fp32 values side by side (packed arithmetic, IEEE per value).
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void split(F2 v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Component values of one weight row (D / 64 = ws) and 16 tokens: h + 128 in
+// the low 16 bits of each word (round_quotient with 128 more in its constant,
+// so that byte 1 is plane hi and byte 0, less 128, plane lo).
+__device__ __forceinline__ void component_values(const int (&v)[16], float ws, const float* z,
+                                                 const float* inv, uint32_t (&h)[16]) {
+  constexpr float kBase = kRound + 128.f;
+  const F2 ws2 = f2(ws, ws), base2 = f2(kBase, kBase), minus2 = f2(-1.f, -1.f);
+  float r[16];
+  bool far = false;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
+    const float4 z4 = *(const float4*)(z + 4 * g), i4 = *(const float4*)(inv + 4 * g);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int e = 4 * g + 2 * u;
+      const F2 z2 = u ? f2(z4.z, z4.w) : f2(z4.x, z4.y), i2 = u ? f2(i4.z, i4.w) : f2(i4.x, i4.y);
+      const F2 p2 = mul2(ws2, f2((float)v[e], (float)v[e + 1]));
+      const F2 y2 = fma2(p2, i2, base2);
+      const F2 r2 = fma2(fma2(y2, minus2, base2), z2, p2);
+      float y0, y1;
+      split(y2, y0, y1);
+      h[e] = __float_as_uint(y0);
+      h[e + 1] = __float_as_uint(y1);
+      split(r2, r[e], r[e + 1]);
+      far = far | (2.f * fabsf(r[e]) >= (u ? z4.z : z4.x)) |
+            (2.f * fabsf(r[e + 1]) >= (u ? z4.w : z4.y));
+    }
+  }
+  if (far) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float twice = 2.f * fabsf(r[e]);
+      if (twice > z[e] || (twice == z[e] && (h[e] & 1u))) h[e] += r[e] > 0.f ? 1u : ~0u;
+    }
+  }
+}
+
+// Those values to the two planes: the four weight rows of the lane and its neighbours
+// and tokens t .. t + 15 (`left` of them exist).  Four lanes trade bytes so
+// that each stores four consecutive rows of one token at once; rows past M
+// fall into the padding of the token's row.
+__device__ __forceinline__ void store_planes(int8_t* y, int64_t ldy, int64_t plane, int left,
+                                             int lane, const uint32_t (&h)[16]) {
+  const uint32_t sel1 = (lane & 1) ? 0x3715u : 0x6240u, sel2 = (lane & 2) ? 0x3276u : 0x5410u;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t* b = h + 4 * g;
+    uint32_t w[2];
+    w[0] = __byte_perm(__byte_perm(b[0], b[1], 0x0051), __byte_perm(b[2], b[3], 0x0051), 0x5410);
+    w[1] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410) ^
+           0x80808080u;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      uint32_t b[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) b[e] = p ? h[4 * g + e] : (h[4 * g + e] + 128u) >> 8;
-      // bytes of tokens 0..3 of this row -> rows of one token, over two exchanges
-      uint32_t w = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-      const uint32_t o1 = __shfl_xor_sync(0xffffffffu, w, 1);
-      w = (lane & 1) ? __byte_perm(w, o1, 0x3715) : __byte_perm(w, o1, 0x6240);
-      const uint32_t o2 = __shfl_xor_sync(0xffffffffu, w, 2);
-      w = (lane & 2) ? __byte_perm(w, o2, 0x3276) : __byte_perm(w, o2, 0x5410);
-      const int tt = t + 4 * g + (lane & 3);
-      if (tt < a.rows && i4 < a.M) {
-        int8_t* y = (int8_t*)a.y + (int64_t)tt * a.ldy + i4 + p * a.plane;
-        *(uint32_t*)y = w;  // (rows past M fall into the padding of the token's row)
-      }
+      // bytes of four tokens of this row -> four rows of one token
+      w[p] = __byte_perm(w[p], __shfl_xor_sync(0xffffffffu, w[p], 1), sel1);
+      w[p] = __byte_perm(w[p], __shfl_xor_sync(0xffffffffu, w[p], 2), sel2);
     }
+    if (4 * g + (lane & 3) < left) {
+      *(uint32_t*)y = w[0];
+      *(uint32_t*)(y + plane) = w[1];
+    }
+    y += 4 * ldy;
   }
 }
 
@@ -266,7 +335,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
   __shared__ __align__(8) Bars bars;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  __shared__ float4 col[2][kAccCols];  // a column's scales
+  // a column's scales: token scale and z, or (planes) z and 1 / z
+  __shared__ __align__(16) float col_a[2][kAccCols], col_b[2][kAccCols];
   constexpr int kEpiWarp0 = epi_warp0(CODES);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int rank = (int)cluster_rank();
@@ -418,20 +488,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
       const int t0 = tt * per;
       // the columns' scales (their buffer's last readers passed the barrier of
       // the tile between)
+      bool odd = false;
       if (et < per) {
         const int t = t0 + et;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t < a.rows) {
-          if (EPI == kOutPlanes)
-            s = component_scale(a.z[t]);
-          else
-            s.x = a.xscale[t], s.y = EPI == kOutFactors ? a.z[t] : 0.f;
+        float s = 0.f, v = 0.f;
+        if (EPI == kOutPlanes) {
+          // a token of zeros, and columns without a token: sums 0, values 0
+          const float z = t < a.rows ? a.z[t] : 0.f;
+          const bool safe = safe_component_scale(z);
+          s = safe ? z : 1.f;
+          v = safe ? __fdiv_rn(1.f, z) : 0.f;
+          odd = z != 0.f && !safe;
+        } else if (t < a.rows) {
+          s = a.xscale[t];
+          if (EPI == kOutFactors) v = a.z[t];
         }
-        col[q][et] = s;
+        col_a[q][et] = s;
+        col_b[q][et] = v;
       }
       const float ws = EPI != kOutFactors && i < a.M ? a.wscale[i] : 0.f;
       const float bias = EPI == kOutDense && a.bias && i < a.M ? a.bias[i] : 0.f;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      // (with the columns' scales in place, whether any of them is not safe)
+      if (EPI == kOutPlanes)
+        odd = bar_any(odd);
+      else
+        asm volatile("bar.sync 1, 256;" ::: "memory");
       bool got = bar_wait(smem_u32(&bars.accf[q]), (seg >> 1) & 1, ab, a.budget);
       if (!__all_sync(0xffffffffu, got)) got = false;
       const bool all_ok = __all_sync(0xffffffffu, got);
@@ -445,35 +526,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
           acc_wait();
           if (EPI == kOutPlanes) {
             uint32_t h[16];
-            bool odd = false;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float4 s = col[q][c0 + e];
-              const float p = ws * (float)(v[e] >> kCodeShift);
-              const Rounded r = round_quotient(p, s.x, s.y);
-              h[e] = settled(r, s.z);
-              odd = odd || s.z < 0.f;
-            }
+            component_values(v, ws * 0.015625f, col_a[q] + c0, col_b[q] + c0, h);
             if (odd) {
-#pragma unroll
               for (int e = 0; e < 16; ++e) {
-                const float4 s = col[q][c0 + e];
-                if (s.z < 0.f)
-                  h[e] = (uint32_t)component_value(ws * (float)(v[e] >> kCodeShift), s.x);
+                const float z = t0 + c0 + e < a.rows ? a.z[t0 + c0 + e] : 0.f;
+                if (z != 0.f && !safe_component_scale(z))
+                  h[e] = (uint32_t)(component_value(ws * (float)(v[e] >> kCodeShift), z) + 128);
               }
             }
-            store_planes(a, h, i, t0 + c0, lane);
+            store_planes((int8_t*)a.y + (int64_t)(t0 + c0 + (lane & 3)) * a.ldy + (i & ~3), a.ldy,
+                         a.plane, (i & ~3) < a.M ? a.rows - (t0 + c0) : 0, lane, h);
           } else {
             float y[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float4 s = col[q][c0 + e];
+              const float s = col_a[q][c0 + e];
               if (EPI == kOutDense) {
                 const float p = ws * (float)v[e];
-                y[e] = a.bias ? fmaf(s.x, p, bias) : s.x * p;
+                y[e] = a.bias ? fmaf(s, p, bias) : s * p;
               } else {
-                y[e] = s.x *
-                       (s.y * fmaf(256.f, (float)(v[e] >> kCodeShift), (float)(lo[e] >> kCodeShift)));
+                // (both sums are multiples of 64 below 2^30: exact as floats)
+                y[e] = s * (col_b[q][c0 + e] * (0.015625f * fmaf(256.f, (float)v[e], (float)lo[e])));
               }
             }
             const int64_t at = (int64_t)(t0 + c0) * a.ldy + i;

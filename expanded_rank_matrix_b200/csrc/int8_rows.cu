@@ -187,30 +187,41 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rows_kernel(cons
   }
 }
 
-// z of rows that are already quantised: one warp a row.
+// z of rows that are already quantised: a CTA a row (long rows) or a warp a
+// row, four 16-byte loads of a thread in flight together.
+template <bool WARP>
 __global__ void __launch_bounds__(256) row_norm_kernel(const int8_t* __restrict__ q, int64_t ldq,
                                                        int64_t rows, int n,
                                                        const float* __restrict__ rho,
                                                        float* __restrict__ z) {
+  __shared__ uint32_t red[32];
   pdl_trigger();
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t row = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
   if (row >= rows) return;
-  const int lane = threadIdx.x & 31;
+  const int G = WARP ? 32 : (int)blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int8_t* x = q + row * ldq;
   int sum = 0;
-  for (int j = lane * 16; j < n; j += 512) {
-    if (j + 16 <= n) {
-      const int4 v = __ldg((const int4*)(x + j));
-      sum = __dp4a(v.x, v.x, sum);
-      sum = __dp4a(v.y, v.y, sum);
-      sum = __dp4a(v.z, v.z, sum);
-      sum = __dp4a(v.w, v.w, sum);
-    } else {
-      for (int e = j; e < n; ++e) sum += (int)x[e] * (int)x[e];
+  for (int j0 = tid * 16; j0 < n; j0 += 4 * G * 16) {
+    int4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u * G * 16;
+      v[u] = make_int4(0, 0, 0, 0);
+      if (j + 16 <= n)
+        v[u] = __ldg((const int4*)(x + j));
+      else
+        for (int e = j; e < n; ++e) sum += (int)x[e] * (int)x[e];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      sum = __dp4a(v[u].x, v[u].x, sum);
+      sum = __dp4a(v[u].y, v[u].y, sum);
+      sum = __dp4a(v[u].z, v[u].z, sum);
+      sum = __dp4a(v[u].w, v[u].w, sum);
     }
   }
-  const uint32_t total = __reduce_add_sync(0xffffffffu, (uint32_t)sum);
-  if (lane == 0) z[row] = (float)((double)__ldg(rho) * sqrt((double)total) / kFullScale);
+  const uint32_t total = group_reduce<WARP, false>((uint32_t)sum, red);
+  if (tid == 0) z[row] = (float)((double)__ldg(rho) * sqrt((double)total) / kFullScale);
 }
 
 template <typename T, int H, bool WARP>
@@ -321,8 +332,12 @@ int quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, int64_t n,
 
 int row_norms(const int8_t* Q, int64_t ldq, int64_t rows, int64_t n, const float* rho, float* z,
               cudaStream_t st) {
-  const int64_t grid = (rows + 7) / 8;
-  row_norm_kernel<<<(unsigned)grid, 256, 0, st>>>(Q, ldq, rows, (int)n, rho, z);
+  if (n <= 2048)
+    row_norm_kernel<true><<<(unsigned)((rows + kWarpRows - 1) / kWarpRows), 32 * kWarpRows, 0, st>>>(
+        Q, ldq, rows, (int)n, rho, z);
+  else
+    row_norm_kernel<false><<<(unsigned)rows, std::min<int>((int)(n + 2047) / 2048 * 32, 256), 0, st>>>(
+        Q, ldq, rows, (int)n, rho, z);
   return cudaGetLastError() == cudaSuccess ? EXTERND_OK : EXTERND_ERR_CUDA;
 }
 
