@@ -26,7 +26,7 @@ constexpr int64_t kPassRows = 4096;
 int64_t type_size(int type) { return type == EXTERND_F32 ? 4 : type == EXTERND_I8 ? 1 : 2; }
 
 int gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st) {
-  return a.rows > 32 ? mma_gemm(a, epi, after_rows, st) : skinny_gemm(a, epi, after_rows, st);
+  return a.rows > kTokens ? mma_gemm(a, epi, after_rows, st) : token_gemm(a, epi, after_rows, st);
 }
 
 // Stream-ordered scratch from the library's pool, freed on the stream.
@@ -67,6 +67,13 @@ int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int
   a.status = status_word_ptr();
   a.budget = kDefaultWaitBudget;
   if (!a.status) return EXTERND_ERR_CUDA;
+  if (rows == 1 && xtype != EXTERND_I8 && n <= kTokenInner) {
+    a.rows = 1;
+    a.y = Y;
+    a.raw = X;
+    a.rawtype = xtype;
+    return token_raw(a, kOutDense, st);
+  }
   Scratch ws(st);
   const int64_t ldq = pad16(n);
   const int64_t chunk = std::min<int64_t>(rows, 65536);
@@ -115,7 +122,15 @@ int factors(const uint32_t* codes_B, const uint32_t* codes_C, const float* D, co
     a.status = status;
     a.budget = kDefaultWaitBudget;
     a.rows = (int)rr;
-    if (xtype == EXTERND_I8) {
+    const bool token = rows == 1 && xtype != EXTERND_I8 && n <= kTokenInner;
+    if (token) {
+      a.raw = X;
+      a.rawtype = xtype;
+      a.rho = rho;
+      a.scale_out = s;
+      a.z_out = z;
+      a.xscale = s;
+    } else if (xtype == EXTERND_I8) {
       a.x = (const int8_t*)X + r0 * ldx;
       a.ldx = ldx;
       a.xscale = xscale + r0;
@@ -132,7 +147,7 @@ int factors(const uint32_t* codes_B, const uint32_t* codes_C, const float* D, co
     a.w = codes_C; a.ldw = code_words(n); a.wscale = D;
     a.M = (int)k; a.K = (int)n;
     a.y = h; a.ldy = ldh; a.plane = plane;
-    rc = gemm(a, kOutPlanes, true, st);
+    rc = token ? token_raw(a, kOutPlanes, st) : gemm(a, kOutPlanes, true, st);
     if (rc != EXTERND_OK) break;
     a.x = h; a.ldx = ldh;
     a.w = codes_B; a.ldw = code_words(k);

@@ -50,6 +50,14 @@ struct GemmArgs {
   int64_t ldy;
   int ytype;
   int rows, M, K;       // tokens, weight rows, inner dimension
+  // a single token that is quantised within the kernel (x, xscale and z above
+  // are not read then): its type, the factors' bound, and where its scale and
+  // z go for the kernel that follows
+  const void* raw;
+  int rawtype;
+  const float* rho;
+  float* scale_out;
+  float* z_out;
   int* status;
   long long budget;
 };

@@ -16,7 +16,13 @@ int row_norms(const int8_t* Q, int64_t ldq, int64_t rows, int64_t n, const float
               cudaStream_t st);
 int pack_codes(const uint32_t* pB, const uint32_t* pC, const float* D, int64_t m, int64_t n,
                int64_t k, uint32_t* codes_B, uint32_t* codes_C, float* rho, cudaStream_t st);
-int skinny_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
+// The products.  after_rows: the launch follows one of this library's kernels
+// on the stream that lets it start early (it waits for that kernel's end
+// before it reads its results).
+constexpr int kTokens = 4;          // most rows of token_gemm
+constexpr int kTokenInner = 32768;  // longest token that token_raw quantises
+int token_raw(const GemmArgs& a, Epilogue epi, cudaStream_t st);
+int token_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
 int mma_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
 int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W, int64_t ldw,
            const float* wscale, const float* bias, int64_t rows, int64_t n, int64_t m, void* Y,

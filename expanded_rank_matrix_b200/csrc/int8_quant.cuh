@@ -1,0 +1,108 @@
+// Quantising a row to 8 bits, for the kernels that do it: reading it in
+// vectors, the bits of its largest magnitude, its scale and its values.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "int8.cuh"
+
+namespace externd {
+namespace i8 {
+
+// Where a thread's vector h lies in the row, and the distance of its elements:
+// aligned rows are read in 16-byte vectors, others an element at a time with
+// neighbouring threads on neighbouring elements.
+template <typename T, bool VEC>
+__device__ __forceinline__ int first_of(int h, int tid, int G) {
+  constexpr int E = 16 / sizeof(T);
+  return VEC ? (h * G + tid) * E : h * G * E + tid;
+}
+
+// E elements from j on (zeros past n)
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_vec(const T* x, int j, int n, int G, T (&v)[16 / sizeof(T)]) {
+  constexpr int E = 16 / sizeof(T);
+  if (VEC && j + E <= n) {
+    *(uint4*)v = __ldg((const uint4*)(x + j));
+  } else {
+    const int step = VEC ? 1 : G;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = j + e * step < n ? x[j + e * step] : T(0.f);
+  }
+}
+
+// Largest magnitude bits seen so far: the bit patterns of non-negative floats
+// order like integers in every type, and a NaN is above infinity.
+__device__ __forceinline__ uint32_t top_bits(uint32_t top, const float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+  return top;
+}
+template <typename T>  // 16-bit types: two magnitudes side by side
+__device__ __forceinline__ uint32_t top_bits(uint32_t top, const T (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = __vmaxu2(top, ((const uint32_t*)v)[e] & 0x7fff7fffu);
+  return top;
+}
+// the magnitude those bits stand for (as fp32 bits)
+__device__ __forceinline__ uint32_t top_value(uint32_t top, float) { return top; }
+template <typename T>
+__device__ __forceinline__ uint32_t top_value(uint32_t top, T) {
+  const uint16_t u = (uint16_t)max(top & 0xffffu, top >> 16);
+  T h;
+  *(uint16_t*)&h = u;
+  return __float_as_uint(to_f32(h)) & 0x7fffffffu;
+}
+
+// Sum or maximum over a warp, or over the CTA; every thread gets it.  `red`
+// is used once in a launch.
+template <bool WARP, bool MAX>
+__device__ __forceinline__ uint32_t group_reduce(uint32_t v, uint32_t* red) {
+  v = MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_add_sync(0xffffffffu, v);
+  if (WARP) return v;
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[wid] = v;
+  __syncthreads();
+  v = lane < (int)(blockDim.x >> 5) ? red[lane] : 0u;
+  return MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_add_sync(0xffffffffu, v);
+}
+
+// The scale of a row from its largest magnitude (as fp32 bits): NaN for a row
+// that is not finite.
+__device__ __forceinline__ float row_scale(uint32_t top) {
+  return top < 0x7f800000u ? __fdiv_rn(__uint_as_float(top), 127.f) : __uint_as_float(0x7fc00000u);
+}
+
+// 8-bit values of E elements, in the low byte of each word.
+template <typename T, int E>
+__device__ __forceinline__ void quantize_vec(const T (&u)[E], float s, float inv, bool safe,
+                                             uint32_t (&b)[E]) {
+  const float half = 0.5f * s;
+  Rounded r[E];
+  float far = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    r[e] = round_quotient(to_f32(u[e]), s, inv);
+    b[e] = low_bits(r[e]);
+    far = fmaxf(far, fabsf(r[e].remainder));
+  }
+  if (!safe) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      // (a subnormal scale may put x / s past 127: the clamp keeps 8 bits)
+      b[e] = s > 0.f ? (uint32_t)max(-127, min(127, nearest_quotient(to_f32(u[e]), s))) : 0u;
+  } else if (far >= half) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) b[e] = settled(r[e], half);
+  }
+}
+
+// four of those words as four bytes
+__device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+}  // namespace i8
+}  // namespace externd

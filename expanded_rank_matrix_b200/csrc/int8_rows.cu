@@ -14,6 +14,7 @@
 #include "common.cuh"
 #include "int8.cuh"
 #include "int8_internal.h"
+#include "int8_quant.cuh"
 #include "internal.h"
 
 namespace externd {
@@ -33,64 +34,6 @@ struct RowArgs {
   int n;
   int* status;
 };
-
-// Where a thread's vector h lies in the row, and the distance of its elements:
-// aligned rows are read in 16-byte vectors, others an element at a time with
-// neighbouring threads on neighbouring elements.
-template <typename T, bool VEC>
-__device__ __forceinline__ int first_of(int h, int tid, int G) {
-  constexpr int E = 16 / sizeof(T);
-  return VEC ? (h * G + tid) * E : h * G * E + tid;
-}
-
-// E elements from j on (zeros past n)
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_vec(const T* x, int j, int n, int G, T (&v)[16 / sizeof(T)]) {
-  constexpr int E = 16 / sizeof(T);
-  if (VEC && j + E <= n) {
-    *(uint4*)v = __ldg((const uint4*)(x + j));
-  } else {
-    const int step = VEC ? 1 : G;
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = j + e * step < n ? x[j + e * step] : T(0.f);
-  }
-}
-
-// Largest magnitude bits seen so far: the bit patterns of non-negative floats
-// order like integers in every type, and a NaN is above infinity.
-__device__ __forceinline__ uint32_t top_bits(uint32_t top, const float (&v)[4]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
-  return top;
-}
-template <typename T>  // 16-bit types: two magnitudes side by side
-__device__ __forceinline__ uint32_t top_bits(uint32_t top, const T (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) top = __vmaxu2(top, ((const uint32_t*)v)[e] & 0x7fff7fffu);
-  return top;
-}
-// the magnitude those bits stand for (as fp32 bits)
-__device__ __forceinline__ uint32_t top_value(uint32_t top, float) { return top; }
-template <typename T>
-__device__ __forceinline__ uint32_t top_value(uint32_t top, T) {
-  const uint16_t u = (uint16_t)max(top & 0xffffu, top >> 16);
-  T h;
-  *(uint16_t*)&h = u;
-  return __float_as_uint(to_f32(h)) & 0x7fffffffu;
-}
-
-// Sum or maximum over a warp, or over the CTA; every thread gets it.  `red`
-// is used once in a launch.
-template <bool WARP, bool MAX>
-__device__ __forceinline__ uint32_t group_reduce(uint32_t v, uint32_t* red) {
-  v = MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_add_sync(0xffffffffu, v);
-  if (WARP) return v;
-  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) red[wid] = v;
-  __syncthreads();
-  v = lane < (int)(blockDim.x >> 5) ? red[lane] : 0u;
-  return MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_add_sync(0xffffffffu, v);
-}
 
 constexpr int kWarpRows = 8;  // rows of a CTA where a warp takes a row
 
@@ -122,9 +65,9 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rows_kernel(cons
   }
   top = group_reduce<WARP, true>(top_value(top, T(0.f)), red[0]);
   const bool finite = top < 0x7f800000u;
-  const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.f) : __uint_as_float(0x7fc00000u);
+  const float s = row_scale(top);
   const bool safe = safe_scale(s);
-  const float inv = safe ? __fdiv_rn(1.f, s) : 0.f, half = 0.5f * s;
+  const float inv = safe ? __fdiv_rn(1.f, s) : 0.f;
   if (tid == 0) {
     a.scale[row] = s;
     if (!finite) atomicCAS(a.status, 0, EXTERND_ERR_NONFINITE);
@@ -133,28 +76,11 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rows_kernel(cons
   uint32_t squares = 0u;
   auto emit = [&](int j, const T (&u)[E]) {
     uint32_t b[E];
-    Rounded r[E];
-    float far = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      r[e] = round_quotient(to_f32(u[e]), s, inv);
-      b[e] = low_bits(r[e]);
-      far = fmaxf(far, fabsf(r[e].remainder));
-    }
-    if (!safe) {
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        // (a subnormal scale may put x / s past 127: the clamp keeps 8 bits)
-        b[e] = s > 0.f ? (uint32_t)max(-127, min(127, nearest_quotient(to_f32(u[e]), s))) : 0u;
-    } else if (far >= half) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) b[e] = settled(r[e], half);
-    }
+    quantize_vec(u, s, inv, safe, b);
     uint32_t packed[E / 4];
 #pragma unroll
     for (int p = 0; p < E / 4; ++p) {
-      packed[p] = __byte_perm(__byte_perm(b[4 * p], b[4 * p + 1], 0x0040),
-                              __byte_perm(b[4 * p + 2], b[4 * p + 3], 0x0040), 0x5410);
+      packed[p] = pack_bytes(b[4 * p], b[4 * p + 1], b[4 * p + 2], b[4 * p + 3]);
       squares = __dp4a((int)packed[p], (int)packed[p], (int)squares);
     }
     if (VEC && j + E <= a.n) {

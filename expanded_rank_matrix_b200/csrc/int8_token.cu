@@ -1,0 +1,288 @@
+// 8-bit products of a few tokens (single ones above all):
+//   dense    y_ti = s_t v_i sum_j q_tj w_ij
+//   planes   h_tc = round(D_c sum_j q_tj C_cj / z_t), as two 8-bit planes
+//   factors  y_ti = s_t z_t sum_c B_ic h_tc
+// Bound by the weights' bytes, and for a single projection by latency: what
+// counts is that every load is on its way at once.  A warp takes R weight rows
+// and its lanes the inner dimension, 16 bytes of a row each (16 8-bit weights,
+// or 64 codes, which unpack in two instructions for four); the products are
+// four-way 8-bit dot products, and a row's 32 partial sums are added by one
+// warp-wide whole-number reduction, so no barrier is needed.  The first
+// weights are requested before the kernel waits for the one in front of it,
+// or quantises its token.
+// (Warp-level 16 x 8 x 32 matrix instructions in their place fill eight columns
+// for one token and took 2.3 us of a 2560 x 7680 factor's product alone.)
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "int8.cuh"
+#include "int8_internal.h"
+#include "int8_quant.cuh"
+#include "internal.h"
+
+namespace externd {
+namespace i8 {
+namespace {
+
+constexpr int kTkThreads = 256;
+
+// the first `left` bytes of 16
+__device__ __forceinline__ uint4 first_bytes(uint4 v, int left) {
+  uint32_t* w = (uint32_t*)&v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int keep = left - 4 * e;
+    w[e] = keep >= 4 ? w[e] : keep <= 0 ? 0u : w[e] & ((1u << (8 * keep)) - 1u);
+  }
+  return v;
+}
+
+// The token's row quantised into shared memory (zeros up to a whole step),
+// its scale, and the sum of its squares; all threads of the CTA take part.
+template <typename T, bool VEC>
+__device__ __forceinline__ float quantize_token(const T* x, int n, int padded, unsigned char* xs,
+                                                uint32_t* red, uint32_t* squares, bool want) {
+  constexpr int E = 16 / sizeof(T);
+  const int G = blockDim.x, tid = threadIdx.x;
+  uint32_t top = 0u;
+#pragma unroll 4
+  for (int h = 0; h * G * E < n; ++h) {
+    T u[E];
+    load_vec<T, VEC>(x, first_of<T, VEC>(h, tid, G), n, G, u);
+    top = top_bits(top, u);
+  }
+  top = group_reduce<false, true>(top_value(top, T(0.f)), red);
+  const float s = row_scale(top);
+  const bool safe = safe_scale(s);
+  const float inv = safe ? __fdiv_rn(1.f, s) : 0.f;
+  uint32_t sq = 0u;
+#pragma unroll 2
+  for (int h = 0; h * G * E < padded; ++h) {
+    const int j = first_of<T, VEC>(h, tid, G);
+    T u[E];
+    uint32_t b[E];
+    load_vec<T, VEC>(x, j, n, G, u);  // (zeros past n: value 0)
+    quantize_vec(u, s, inv, safe, b);
+#pragma unroll
+    for (int p = 0; p < E / 4; ++p) {
+      const uint32_t w = pack_bytes(b[4 * p], b[4 * p + 1], b[4 * p + 2], b[4 * p + 3]);
+      if (want) sq = __dp4a((int)w, (int)w, (int)sq);
+      if (VEC) {
+        if (j + 4 * p < padded) *(uint32_t*)(xs + j + 4 * p) = w;
+      } else {
+#pragma unroll
+        for (int e = 4 * p; e < 4 * p + 4; ++e)
+          if (j + e * G < padded) xs[j + e * G] = (unsigned char)b[e];
+      }
+    }
+  }
+  if (want) *squares = group_reduce<false, false>(sq, red + 32);
+  return s;
+}
+
+// A lane's weights of a step: 16 entries, as bytes or as codes.  The step's 512
+// entries are neighbours across the lanes, so weights and activations both
+// come in whole lines (64 codes a lane would spread a warp's activation load
+// over 16 lines).
+template <bool CODES>
+struct Weights {
+  typedef uint4 type;
+};
+template <>
+struct Weights<true> {
+  typedef uint32_t type;
+};
+constexpr int kEntries = 16, kSpan = 32 * kEntries;
+
+__device__ __forceinline__ uint32_t four(const uint4& w, int e) { return ((const uint32_t*)&w)[e]; }
+__device__ __forceinline__ uint32_t four(const uint32_t& w, int e) { return (w << (2 * e)) & kCodeMask; }
+
+// T tokens (columns past the last repeat it and are not stored), R rows a
+// warp, U steps of loads in flight.  RAW: the type of a single token that the
+// kernel quantises itself (every CTA the whole row: a launch less), or int8_t.
+template <bool CODES, Epilogue EPI, int R, int T, typename RAW, bool VEC>
+__global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
+  constexpr int P = EPI == kOutFactors ? 2 : 1;  // planes of the activations
+  constexpr bool FUSED = sizeof(RAW) > 1;
+  constexpr int U = CODES ? 5 : R == 4 ? 5 : 8;
+  typedef typename Weights<CODES>::type W;
+  __shared__ uint32_t rowred[FUSED ? 64 : 1];
+  extern __shared__ __align__(16) unsigned char xs[];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int i0 = (blockIdx.x * (blockDim.x >> 5) + (tid >> 5)) * R;
+  const char* w[R];  // (rows past M repeat the last one)
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    w[r] = (const char*)a.w + (int64_t)min(i0 + r, a.M - 1) * a.ldw * (CODES ? 4 : 1) +
+           sizeof(W) * lane;
+  W c[U][R];
+  auto fetch = [&](int k) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = k + u * kSpan;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        c[u][r] = W();
+        if (at + lane * kEntries < a.K)
+          c[u][r] = __ldg((const W*)(w[r] + at / kEntries * (int)sizeof(W)));
+      }
+    }
+  };
+  fetch(0);
+  pdl_trigger();
+  pdl_wait();
+  float scale = 0.f, z = 0.f;
+  if constexpr (FUSED) {
+    uint32_t squares = 0u;
+    scale = quantize_token<RAW, VEC>((const RAW*)a.raw, a.K, (a.K + 15) / 16 * 16, xs, rowred,
+                                     &squares, EPI == kOutPlanes);
+    if (EPI == kOutPlanes)
+      z = (float)((double)__ldg(a.rho) * sqrt((double)squares) / kFullScale);
+    if (blockIdx.x == 0 && tid == 0) {
+      if (EPI == kOutPlanes) a.scale_out[0] = scale, a.z_out[0] = z;
+      if (isnan(scale)) atomicCAS(a.status, 0, EXTERND_ERR_NONFINITE);
+    }
+    __syncthreads();
+  }
+  int acc[R][T][P];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int p = 0; p < P; ++p) acc[r][t][p] = 0;
+  for (int k = 0; k < a.K; k += U * kSpan) {
+    if (k) fetch(k);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const int8_t* xp = FUSED ? nullptr : a.x + (int64_t)min(t, a.rows - 1) * a.ldx;
+      uint4 x[U][P];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int kk = k + u * kSpan + lane * kEntries;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          x[u][p] = make_uint4(0u, 0u, 0u, 0u);
+          if (kk < a.K)
+            x[u][p] = FUSED ? *(const uint4*)(xs + kk) : __ldg((const uint4*)(xp + p * a.plane + kk));
+        }
+      }
+      if (!FUSED && k + U * kSpan > a.K) {  // rows may be padded with anything past K
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            x[u][p] = first_bytes(x[u][p], a.K - (k + u * kSpan + lane * kEntries));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t v = four(c[u][r], e);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+              acc[r][t][p] = __dp4a((int)v, (int)((const uint32_t*)&x[u][p])[e], acc[r][t][p]);
+          }
+    }
+  }
+  // lane r + R t finishes row r of token t
+  int sum[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) sum[p] = 0;
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int v = __reduce_add_sync(0xffffffffu, acc[r][t][p]);
+        if (lane == r + R * t) sum[p] = v;
+      }
+  const int i = i0 + (lane & (R - 1)), t = lane / R;
+  if (t >= T || t >= a.rows || i >= a.M) return;
+  if (CODES) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) sum[p] >>= kCodeShift;
+  }
+  if (EPI == kOutDense) {
+    const float sx = FUSED ? scale : a.xscale[t], v = a.wscale[i] * (float)sum[0];
+    store_out(a.y, (int64_t)t * a.ldy + i, a.ytype, a.bias ? fmaf(sx, v, a.bias[i]) : sx * v);
+  } else if (EPI == kOutPlanes) {
+    const int h = component_value(a.wscale[i] * (float)sum[0], FUSED ? z : a.z[t]);
+    const int hi = (h + 128) >> 8;
+    int8_t* y = (int8_t*)a.y + (int64_t)t * a.ldy + i;
+    y[0] = (int8_t)hi;
+    y[a.plane] = (int8_t)(h - 256 * hi);
+  } else {
+    const float v = fmaf(256.f, (float)sum[0], (float)sum[P - 1]);
+    store_out(a.y, (int64_t)t * a.ldy + i, a.ytype, a.xscale[t] * (a.z[t] * v));
+  }
+}
+
+template <bool CODES, Epilogue EPI, int R, int T, typename RAW, bool VEC>
+int launch_r(const GemmArgs& a, bool after_rows, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.M + R * kTkThreads / 32 - 1) / (R * kTkThreads / 32)));
+  cfg.blockDim = dim3(kTkThreads);
+  cfg.dynamicSmemBytes = sizeof(RAW) > 1 ? (a.K + 15) / 16 * 16 : 0;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = after_rows ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, token_kernel<CODES, EPI, R, T, RAW, VEC>, a) != cudaSuccess) {
+    cudaGetLastError();
+    return EXTERND_ERR_CUDA;
+  }
+  return EXTERND_OK;
+}
+
+// More rows a warp reuse a lane's activations; fewer keep all SMs at work.
+template <bool CODES, Epilogue EPI, int T, typename RAW, bool VEC>
+int launch(const GemmArgs& a, bool after_rows, cudaStream_t st) {
+  if (a.M >= 8192) return launch_r<CODES, EPI, 4, T, RAW, VEC>(a, after_rows, st);
+  if (a.M >= 4096) return launch_r<CODES, EPI, 2, T, RAW, VEC>(a, after_rows, st);
+  return launch_r<CODES, EPI, 1, T, RAW, VEC>(a, after_rows, st);
+}
+
+template <bool CODES, Epilogue EPI>
+int launch_i8(const GemmArgs& a, bool after_rows, cudaStream_t st) {
+  if (a.rows == 1) return launch<CODES, EPI, 1, int8_t, true>(a, after_rows, st);
+  if (a.rows == 2) return launch<CODES, EPI, 2, int8_t, true>(a, after_rows, st);
+  return launch<CODES, EPI, 4, int8_t, true>(a, after_rows, st);
+}
+
+template <bool CODES, Epilogue EPI, typename RAW>
+int launch_raw(const GemmArgs& a, cudaStream_t st) {
+  return ((uintptr_t)a.raw & 15) == 0 ? launch<CODES, EPI, 1, RAW, true>(a, false, st)
+                                      : launch<CODES, EPI, 1, RAW, false>(a, false, st);
+}
+
+template <bool CODES, Epilogue EPI>
+int launch_token(const GemmArgs& a, cudaStream_t st) {
+  if (a.rawtype == EXTERND_BF16) return launch_raw<CODES, EPI, __nv_bfloat16>(a, st);
+  if (a.rawtype == EXTERND_F16) return launch_raw<CODES, EPI, __half>(a, st);
+  return launch_raw<CODES, EPI, float>(a, st);
+}
+
+}  // namespace
+
+int token_raw(const GemmArgs& a, Epilogue epi, cudaStream_t st) {
+  return epi == kOutDense ? launch_token<false, kOutDense>(a, st)
+                          : launch_token<true, kOutPlanes>(a, st);
+}
+
+int token_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st) {
+  if (epi == kOutDense) return launch_i8<false, kOutDense>(a, after_rows, st);
+  if (epi == kOutPlanes) return launch_i8<true, kOutPlanes>(a, after_rows, st);
+  return launch_i8<true, kOutFactors>(a, after_rows, st);
+}
+
+}  // namespace i8
+}  // namespace externd
