@@ -170,8 +170,7 @@ int externd_quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, in
   if (rows == 0) return EXTERND_OK;
   if (!float_matrix_ok(X, type, ldx, n) || !bytes_matrix_ok(Q, ldq, n) || !scale || !aligned4(scale))
     return EXTERND_ERR_INVALID_ARG;
-  return externd::i8::quantize_rows(X, type, ldx, rows, n, Q, ldq, scale, nullptr, nullptr,
-                                    (cudaStream_t)stream);
+  return externd::i8::quantize(X, type, ldx, rows, n, Q, ldq, scale, (cudaStream_t)stream);
 }
 
 int externd_matmul_i8(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W,

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "common.cuh"
@@ -27,6 +28,20 @@ int64_t type_size(int type) { return type == EXTERND_F32 ? 4 : type == EXTERND_I
 
 int gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st) {
   return a.rows > kTokens ? mma_gemm(a, epi, after_rows, st) : token_gemm(a, epi, after_rows, st);
+}
+
+// The device's status word (its address does not change; looking it up costs
+// as much as a small launch's arguments).
+int* status_word() {
+  static std::atomic<int*> at[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  int* p = at[dev].load(std::memory_order_relaxed);
+  if (!p) {
+    p = status_word_ptr();
+    at[dev].store(p, std::memory_order_relaxed);
+  }
+  return p;
 }
 
 // Stream-ordered scratch from the library's pool, freed on the stream.
@@ -57,6 +72,13 @@ struct Scratch {
 
 }  // namespace
 
+int quantize(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8_t* Q, int64_t ldq,
+             float* scale, cudaStream_t st) {
+  int* status = status_word();
+  if (!status) return EXTERND_ERR_CUDA;
+  return quantize_rows(X, type, ldx, rows, n, Q, ldq, scale, nullptr, nullptr, status, st);
+}
+
 int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W, int64_t ldw,
            const float* wscale, const float* bias, int64_t rows, int64_t n, int64_t m, void* Y,
            int ytype, int64_t ldy, cudaStream_t st) {
@@ -64,7 +86,7 @@ int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int
   a.w = W; a.ldw = ldw; a.wscale = wscale; a.bias = bias;
   a.ytype = ytype; a.ldy = ldy;
   a.M = (int)m; a.K = (int)n;
-  a.status = status_word_ptr();
+  a.status = status_word();
   a.budget = kDefaultWaitBudget;
   if (!a.status) return EXTERND_ERR_CUDA;
   if (rows == 1 && xtype != EXTERND_I8 && n <= kTokenInner) {
@@ -90,7 +112,7 @@ int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int
     } else {
       float* s = (float*)(ws.p + chunk * ldq);
       rc = quantize_rows((const char*)X + r0 * ldx * type_size(xtype), xtype, ldx, rr, n,
-                         (int8_t*)ws.p, ldq, s, nullptr, nullptr, st);
+                         (int8_t*)ws.p, ldq, s, nullptr, nullptr, a.status, st);
       a.x = (const int8_t*)ws.p;
       a.ldx = ldq;
       a.xscale = s;
@@ -103,7 +125,7 @@ int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int
 int factors(const uint32_t* codes_B, const uint32_t* codes_C, const float* D, const float* rho,
             int64_t m, int64_t n, int64_t k, const void* X, int xtype, int64_t ldx,
             const float* xscale, int64_t rows, void* Y, int ytype, int64_t ldy, cudaStream_t st) {
-  int* status = status_word_ptr();
+  int* status = status_word();
   if (!status) return EXTERND_ERR_CUDA;
   const int64_t chunk = std::min(rows, kPassRows);
   const int64_t ldq = pad16(n), ldh = pad16(k);
@@ -137,7 +159,7 @@ int factors(const uint32_t* codes_B, const uint32_t* codes_C, const float* D, co
       rc = row_norms(a.x, ldx, rr, n, rho, z, st);
     } else {
       rc = quantize_rows((const char*)X + r0 * ldx * type_size(xtype), xtype, ldx, rr, n, q, ldq, s,
-                         rho, z, st);
+                         rho, z, status, st);
       a.x = q;
       a.ldx = ldq;
       a.xscale = s;

@@ -11,7 +11,7 @@ namespace i8 {
 
 // Q, scale from X; with rho also z = fl(rho |q|_2 / 32512) of each row.
 int quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8_t* Q,
-                  int64_t ldq, float* scale, const float* rho, float* z, cudaStream_t st);
+                  int64_t ldq, float* scale, const float* rho, float* z, int* status, cudaStream_t st);
 int row_norms(const int8_t* Q, int64_t ldq, int64_t rows, int64_t n, const float* rho, float* z,
               cudaStream_t st);
 int pack_codes(const uint32_t* pB, const uint32_t* pC, const float* D, int64_t m, int64_t n,
@@ -24,6 +24,8 @@ constexpr int kTokenInner = 32768;  // longest token that token_raw quantises
 int token_raw(const GemmArgs& a, Epilogue epi, cudaStream_t st);
 int token_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
 int mma_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
+int quantize(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8_t* Q, int64_t ldq,
+             float* scale, cudaStream_t st);
 int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W, int64_t ldw,
            const float* wscale, const float* bias, int64_t rows, int64_t n, int64_t m, void* Y,
            int ytype, int64_t ldy, cudaStream_t st);

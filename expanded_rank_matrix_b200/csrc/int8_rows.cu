@@ -180,12 +180,11 @@ int launch_rows(const RowArgs<T>& a, cudaStream_t st) {
 
 template <typename T>
 int rows_of(const void* x, int64_t ldx, int64_t rows, int64_t n, int8_t* q, int64_t ldq,
-            float* scale, const float* rho, float* z, cudaStream_t st) {
+            float* scale, const float* rho, float* z, int* status, cudaStream_t st) {
   RowArgs<T> a = {};
   a.x = (const T*)x; a.ldx = ldx; a.q = q; a.ldq = ldq; a.scale = scale; a.rho = rho; a.z = z;
   a.rows = rows; a.n = (int)n;
-  a.status = status_word_ptr();
-  if (!a.status) return EXTERND_ERR_CUDA;
+  a.status = status;
   return launch_rows<T>(a, st);
 }
 
@@ -249,11 +248,11 @@ __global__ void __launch_bounds__(256) pack_c_kernel(const uint32_t* __restrict_
 }  // namespace
 
 int quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8_t* Q,
-                  int64_t ldq, float* scale, const float* rho, float* z, cudaStream_t st) {
+                  int64_t ldq, float* scale, const float* rho, float* z, int* status, cudaStream_t st) {
   if (type == EXTERND_BF16)
-    return rows_of<__nv_bfloat16>(X, ldx, rows, n, Q, ldq, scale, rho, z, st);
-  if (type == EXTERND_F16) return rows_of<__half>(X, ldx, rows, n, Q, ldq, scale, rho, z, st);
-  return rows_of<float>(X, ldx, rows, n, Q, ldq, scale, rho, z, st);
+    return rows_of<__nv_bfloat16>(X, ldx, rows, n, Q, ldq, scale, rho, z, status, st);
+  if (type == EXTERND_F16) return rows_of<__half>(X, ldx, rows, n, Q, ldq, scale, rho, z, status, st);
+  return rows_of<float>(X, ldx, rows, n, Q, ldq, scale, rho, z, status, st);
 }
 
 int row_norms(const int8_t* Q, int64_t ldq, int64_t rows, int64_t n, const float* rho, float* z,

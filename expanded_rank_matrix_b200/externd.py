@@ -322,21 +322,167 @@ F32, F16, BF16, I8 = 0, 1, 2, 3
 _TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
 
-@dataclass
+def _device_of(t: torch.Tensor, *others) -> int:
+    """The index of the one CUDA device that holds all of these tensors."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("expected a CUDA tensor")
+    for o in others:
+        if o is not None and o.get_device() != index:
+            raise ValueError("expected tensors on one CUDA device")
+    return index
+
+
+def _elsewhere(index: int, stream: Optional[torch.cuda.Stream]) -> bool:
+    """Whether a call has to change the current device or stream first (_on)."""
+    return stream is not None or index != torch._C._cuda_getDevice()
+
+
+def _on(index: int, stream: Optional[torch.cuda.Stream]):
+    """Context in which the tensors' device, and a given stream, are current:
+    what is allocated or copied inside belongs to the stream of the launch."""
+    if stream is None:
+        return torch.cuda.device(index)
+    if stream.device_index != index:
+        raise ValueError("the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream)
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _matrix(X: torch.Tensor):
+    """(matrix of X's rows, distance between rows): X [..., n] itself where its
+    rows lie at one distance and their elements side by side, else a copy."""
+    M = X if X.dim() == 2 else X.reshape(-1, X.shape[-1])
+    rows, n = M.shape
+    if (n > 1 and M.stride(1) != 1) or (rows > 1 and M.stride(0) < n):
+        M = M.contiguous()
+    # (the stride of a single row means nothing)
+    return M, M.stride(0) if rows > 1 else n
+
+
+def _vector(v: torch.Tensor, length: int, what: str) -> torch.Tensor:
+    if v.dtype != torch.float32 or v.dim() != 1 or v.shape[0] != length:
+        raise ValueError(f"{what} must be fp32 [{length}]")
+    return v if v.is_contiguous() else v.contiguous()
+
+
+@dataclass(frozen=True)
 class Quantized:
     """Rows in 8 bits with one scale a row: row i stands for q[i] * scale[i].
-    q is int8 [rows, n] whose rows start on 16-byte boundaries and hold
-    readable storage up to the next one (as quantize_rows allocates it);
-    scale is fp32 [rows].  Any other int8 matrix is copied into that form
-    when it is used."""
+    q: int8 [rows, n], scale: fp32 [rows], on one CUDA device.  The rows of q
+    start on 16-byte boundaries, each in storage up to the next boundary, as
+    quantize_rows allocates them; a q in any other layout is copied into this
+    one here, when the object is made."""
     q: torch.Tensor
     scale: torch.Tensor
 
+    def __post_init__(self):
+        q = self.q
+        if q.dtype != torch.int8 or q.dim() != 2:
+            raise ValueError("q must be a 2-D int8 tensor")
+        rows, n = q.shape
+        ld = q.stride(0) if rows > 1 else (n + 15) // 16 * 16
+        end = q.storage_offset() + max(rows - 1, 0) * ld + (n + 15) // 16 * 16
+        if not ((n == 1 or q.stride(1) == 1) and ld % 16 == 0 and ld >= n
+                and q.data_ptr() % 16 == 0 and end <= q.untyped_storage().nbytes()):
+            ld = (n + 15) // 16 * 16
+            out = torch.empty((rows, ld), dtype=torch.int8, device=q.device)[:, :n]
+            out.copy_(q)
+            q = out
+        self._set(q, _vector(self.scale, rows, "scale"), ld, _device_of(q, self.scale))
 
-@dataclass
+    def _set(self, q, scale, ld, device):
+        d = self.__dict__
+        d["q"], d["scale"], d["_ld"], d["_device"] = q, scale, ld, device
+
+
+def quantize_rows(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> Quantized:
+    """Symmetric 8-bit quantisation of the rows of X [..., n] (fp32, fp16 or
+    bf16) with one scale a row (externd_quantize_rows): tokens of activations,
+    output channels of a weight matrix."""
+    kind = _TYPES.get(X.dtype)
+    if kind is None or X.dim() == 0:
+        raise ValueError("X must be an fp32, fp16 or bf16 tensor of at least one dimension")
+    device = _device_of(X)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return quantize_rows(X)
+    M, ldx = _matrix(X)
+    rows, n = M.shape
+    ldq = (n + 15) // 16 * 16
+    q = M.new_empty((rows, ldq), dtype=torch.int8)
+    scale = M.new_empty(rows, dtype=torch.float32)
+    rc = load().externd_quantize_rows(M.data_ptr(), kind, ldx, rows, n, q.data_ptr(), ldq,
+                                      scale.data_ptr(), _raw_stream(device))
+    if rc != OK:
+        raise ExterndError(rc, "externd_quantize_rows")
+    out = Quantized.__new__(Quantized)
+    out._set(q if ldq == n else q[:, :n], scale, ldq, device)
+    return out
+
+
+def _activations(X, n: int, device: int, out_dtype):
+    """(matrix, its scales' address, type, row distance, leading sizes, output
+    type) of the activations of an 8-bit product."""
+    if X.__class__ is Quantized:
+        M, s, kind, ldx, lead = X.q, X.scale.data_ptr(), I8, X._ld, X.q.shape[:1]
+        where, dt = X._device, out_dtype or torch.float32
+    else:
+        kind = _TYPES.get(X.dtype)
+        if kind is None or X.dim() == 0:
+            raise ValueError("X must be Quantized, or an fp32, fp16 or bf16 tensor of at least "
+                             "one dimension")
+        (M, ldx), s, lead = _matrix(X), None, X.shape[:-1]
+        where, dt = X.get_device(), out_dtype or X.dtype
+    if where != device:
+        raise ValueError("expected tensors on one CUDA device")
+    if M.shape[1] != n:
+        raise ValueError(f"X must have {n} columns")
+    if dt not in _TYPES:
+        raise ValueError("out_dtype must be fp32, fp16 or bf16")
+    return M, s, kind, ldx, lead, dt
+
+
+def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=None,
+              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """X W^T (+ bias) with 8-bit operands and whole-number sums, one scale for
+    each token and each output channel (externd_matmul_i8).  X: [..., n] fp32,
+    fp16 or bf16, quantised within the call, or Quantized rows (shared by
+    several products).  The output is [..., m] of out_dtype (default: X's
+    type; fp32 for Quantized)."""
+    device = W._device
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return matmul_i8(X, W, bias, out_dtype)
+    m, n = W.q.shape
+    M, s, kind, ldx, lead, dt = _activations(X, n, device, out_dtype)
+    b = None
+    if bias is not None:
+        bias = _vector(bias, m, "bias")
+        if bias.get_device() != device:
+            raise ValueError("expected tensors on one CUDA device")
+        b = bias.data_ptr()
+    Y = M.new_empty((*lead, m), dtype=dt)
+    rc = load().externd_matmul_i8(M.data_ptr(), kind, ldx, s, W.q.data_ptr(), W._ld,
+                                  W.scale.data_ptr(), b, M.shape[0], n, m, Y.data_ptr(),
+                                  _TYPES[dt], m, _raw_stream(device))
+    if rc != OK:
+        raise ExterndError(rc, "externd_matmul_i8")
+    return Y
+
+
+def code_words(length: int) -> int:
+    """32-bit words of one row of packed ternary codes."""
+    return int(load().externd_code_words(length))
+
+
+@dataclass(frozen=True)
 class FactorCodes:
-    """Factors laid out for apply_i8 (pack_codes): two-bit codes, B row by row
-    and C component by component, D, and the bound of the component sums."""
+    """Factors laid out for apply_i8, as pack_codes returns them: two-bit codes,
+    B row by row and C component by component, D, and the bound of the
+    component sums."""
     codes_B: torch.Tensor  # int32 view of uint32 [m, code_words(k)]
     codes_C: torch.Tensor  # [k, code_words(n)]
     D: torch.Tensor        # fp32 [k]
@@ -348,171 +494,35 @@ class FactorCodes:
     def k(self) -> int:
         return int(self.D.shape[0])
 
-
-def code_words(length: int) -> int:
-    """32-bit words of one row of packed ternary codes."""
-    return int(load().externd_code_words(length))
-
-
-class _On:
-    """Makes a tensor's device, and a given stream, the current ones, so that
-    allocations and copies made inside belong to the stream of the launch."""
-
-    def __init__(self, index: int, stream: Optional[torch.cuda.Stream]):
-        if stream is not None and stream.device_index != index:
-            raise ValueError("the stream belongs to another device than the tensors")
-        self._ctx = None
-        if stream is not None:
-            self._ctx = torch.cuda.stream(stream)
-        elif index != torch.cuda.current_device():
-            self._ctx = torch.cuda.device(index)
-        self.index = index
-
-    def __enter__(self) -> int:
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        return False
-
-
-def _device_index(t: torch.Tensor, *others) -> int:
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    index = t.get_device()
-    for o in others:
-        if o is not None and (not o.is_cuda or o.get_device() != index):
-            raise ValueError("expected tensors on one CUDA device")
-    return index
-
-
-def _matrix(X: torch.Tensor) -> torch.Tensor:
-    """X [..., n] as a matrix of rows, without a copy where its rows lie at
-    one distance and their elements side by side."""
-    if X.dim() == 0:
-        raise ValueError("expected at least one dimension")
-    M = X if X.dim() == 2 else X.reshape(-1, X.shape[-1])
-    rows, n = M.shape
-    if (n > 1 and M.stride(1) != 1) or (rows > 1 and M.stride(0) < n):
-        M = M.contiguous()
-    return M
-
-
-def _ld(M: torch.Tensor) -> int:
-    # (the stride of a single row means nothing)
-    return M.stride(0) if M.shape[0] > 1 else max(M.shape[1], 1)
-
-
-def _aligned_rows(q: torch.Tensor) -> torch.Tensor:
-    """An int8 matrix whose rows start on 16-byte boundaries within storage
-    that holds every row up to the next one: q itself, or a copy."""
-    if q.dtype != torch.int8 or q.dim() != 2:
-        raise ValueError("expected a 2-D int8 tensor")
-    rows, n = q.shape
-    if rows == 0 or n == 0:
-        return q
-    ld = q.stride(0) if rows > 1 else (n + 15) // 16 * 16
-    end = q.storage_offset() + (rows - 1) * ld + (n + 15) // 16 * 16
-    if ((n == 1 or q.stride(1) == 1) and q.data_ptr() % 16 == 0 and ld % 16 == 0 and ld >= n
-            and end <= q.untyped_storage().nbytes()):
-        return q
-    out = torch.empty((rows, (n + 15) // 16 * 16), dtype=torch.int8, device=q.device)[:, :n]
-    out.copy_(q)
-    return out
-
-
-def _ld_bytes(q: torch.Tensor) -> int:
-    return q.stride(0) if q.shape[0] > 1 else (q.shape[1] + 15) // 16 * 16
-
-
-def _vector(v: torch.Tensor, length: int, what: str) -> torch.Tensor:
-    if v.dtype != torch.float32 or v.dim() != 1 or v.shape[0] != length:
-        raise ValueError(f"{what} must be fp32 [{length}]")
-    return v.contiguous()
-
-
-def quantize_rows(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> Quantized:
-    """Symmetric 8-bit quantisation of the rows of X [..., n] (fp32, fp16 or
-    bf16) with one scale a row (externd_quantize_rows): tokens of activations,
-    output channels of a weight matrix."""
-    if X.dtype not in _TYPES:
-        raise ValueError("X must be fp32, fp16 or bf16")
-    with _On(_device_index(X), stream) as st:
-        M = _matrix(X)
-        rows, n = M.shape
-        ldq = (n + 15) // 16 * 16
-        q = torch.empty((rows, ldq), dtype=torch.int8, device=X.device)
-        scale = torch.empty(rows, dtype=torch.float32, device=X.device)
-        rc = load().externd_quantize_rows(M.data_ptr(), _TYPES[X.dtype], _ld(M), rows, n,
-                                          q.data_ptr(), ldq, scale.data_ptr(), st)
-    if rc != OK:
-        raise ExterndError(rc, "externd_quantize_rows")
-    return Quantized(q if ldq == n else q[:, :n], scale)
-
-
-def _activations(X, n: int, out_dtype):
-    """(matrix, scales, type, row distance, leading shape, output type)."""
-    if isinstance(X, Quantized):
-        q = _aligned_rows(X.q)
-        s = _vector(X.scale, q.shape[0], "scale")
-        if q.shape[1] != n:
-            raise ValueError(f"X must have {n} columns")
-        return q, s, I8, _ld_bytes(q), (q.shape[0],), out_dtype or torch.float32
-    if X.dtype not in _TYPES:
-        raise ValueError("X must be fp32, fp16, bf16 or Quantized")
-    M = _matrix(X)
-    if M.shape[1] != n:
-        raise ValueError(f"X must have {n} columns")
-    return M, None, _TYPES[X.dtype], _ld(M), X.shape[:-1], out_dtype or X.dtype
-
-
-def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=None,
-              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
-    """X W^T (+ bias) with 8-bit operands and whole-number sums, one scale for
-    each token and each output channel (externd_matmul_i8).  X: [..., n] fp32,
-    fp16 or bf16, quantised within the call, or Quantized rows (shared by
-    several products).  The output is [..., m] of out_dtype (default: X's
-    type; fp32 for Quantized)."""
-    x = X.q if isinstance(X, Quantized) else X
-    with _On(_device_index(x, X.scale if isinstance(X, Quantized) else None, W.q, W.scale, bias),
-             stream) as st:
-        w = _aligned_rows(W.q)
-        m, n = w.shape
-        ws = _vector(W.scale, m, "scale")
-        b = None if bias is None else _vector(bias, m, "bias")
-        M, s, xtype, ldx, lead, dt = _activations(X, n, out_dtype)
-        if dt not in _TYPES:
-            raise ValueError("out_dtype must be fp32, fp16 or bf16")
-        rows = M.shape[0]
-        Y = torch.empty((*lead, m), dtype=dt, device=M.device)
-        rc = load().externd_matmul_i8(M.data_ptr(), xtype, ldx, None if s is None else s.data_ptr(),
-                                      w.data_ptr(), _ld_bytes(w), ws.data_ptr(),
-                                      None if b is None else b.data_ptr(), rows, n, m,
-                                      Y.data_ptr(), _TYPES[dt], m, st)
-    if rc != OK:
-        raise ExterndError(rc, "externd_matmul_i8")
-    return Y
+    def __post_init__(self):
+        k = self.k
+        for t, shape, kind in ((self.codes_B, (self.m, code_words(k)), torch.int32),
+                               (self.codes_C, (k, code_words(self.n)), torch.int32),
+                               (self.D, (k,), torch.float32), (self.bound, (1,), torch.float32)):
+            if t.dtype != kind or t.shape != shape or not t.is_contiguous():
+                raise ValueError("codes, D and bound must be as pack_codes returns them")
+        self.__dict__["_device"] = _device_of(self.D, self.codes_B, self.codes_C, self.bound)
 
 
 def pack_codes(f: Factors, stream: Optional[torch.cuda.Stream] = None) -> FactorCodes:
-    """Lays factors out once for apply_i8 (externd_pack_codes).  The factors
-    of a decomposition, or some of its components (truncate)."""
-    with _On(_device_index(f.D, f.packed_B, f.packed_C), stream) as st:
-        dev, k = f.D.device, f.k
-        D = f.D.contiguous()
-        pB, pC = f.packed_B.contiguous(), f.packed_C.contiguous()
-        if pB.shape != (k, 2, words(f.m)) or pC.shape != (k, 2, words(f.n)):
-            raise ValueError("packed factors and D do not belong together")
-        if (pB.dtype, pC.dtype, D.dtype) != (torch.int32, torch.int32, torch.float32):
-            raise ValueError("packed factors must be int32 and D fp32")
-        cB = torch.empty((f.m, code_words(k)), dtype=torch.int32, device=dev)
-        cC = torch.empty((k, code_words(f.n)), dtype=torch.int32, device=dev)
-        bound = torch.empty(1, dtype=torch.float32, device=dev)
-        rc = load().externd_pack_codes(pB.data_ptr(), pC.data_ptr(), D.data_ptr(), f.m, f.n, k,
-                                       cB.data_ptr(), cC.data_ptr(), bound.data_ptr(), st)
+    """Lays factors out once for apply_i8 (externd_pack_codes): those of a
+    decomposition, or its first components (truncate)."""
+    device = _device_of(f.D, f.packed_B, f.packed_C)
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return pack_codes(f)
+    k = f.k
+    D, pB, pC = f.D.contiguous(), f.packed_B.contiguous(), f.packed_C.contiguous()
+    if pB.shape != (k, 2, words(f.m)) or pC.shape != (k, 2, words(f.n)):
+        raise ValueError("packed factors and D do not belong together")
+    if (pB.dtype, pC.dtype, D.dtype) != (torch.int32, torch.int32, torch.float32):
+        raise ValueError("packed factors must be int32 and D fp32")
+    cB = D.new_empty((f.m, code_words(k)), dtype=torch.int32)
+    cC = D.new_empty((k, code_words(f.n)), dtype=torch.int32)
+    bound = D.new_empty(1)
+    rc = load().externd_pack_codes(pB.data_ptr(), pC.data_ptr(), D.data_ptr(), f.m, f.n, k,
+                                   cB.data_ptr(), cC.data_ptr(), bound.data_ptr(),
+                                   _raw_stream(device))
     if rc != OK:
         raise ExterndError(rc, "externd_pack_codes")
     return FactorCodes(cB, cC, D, bound, f.m, f.n)
@@ -522,17 +532,16 @@ def apply_i8(c: FactorCodes, X, out_dtype=None,
              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """X (B diag(D) C)^T on 8-bit activations, from the packed codes
     (externd_ternary_apply_i8).  X and out_dtype as for matmul_i8."""
-    x = X.q if isinstance(X, Quantized) else X
-    with _On(_device_index(x, X.scale if isinstance(X, Quantized) else None, c.D, c.codes_B,
-                           c.codes_C, c.bound), stream) as st:
-        M, s, xtype, ldx, lead, dt = _activations(X, c.n, out_dtype)
-        if dt not in _TYPES:
-            raise ValueError("out_dtype must be fp32, fp16 or bf16")
-        Y = torch.empty((*lead, c.m), dtype=dt, device=M.device)
-        rc = load().externd_ternary_apply_i8(
-            c.codes_B.data_ptr(), c.codes_C.data_ptr(), c.D.data_ptr(), c.bound.data_ptr(), c.m,
-            c.n, c.D.shape[0], M.data_ptr(), xtype, ldx, None if s is None else s.data_ptr(),
-            M.shape[0], Y.data_ptr(), _TYPES[dt], c.m, st)
+    device = c._device
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return apply_i8(c, X, out_dtype)
+    M, s, kind, ldx, lead, dt = _activations(X, c.n, device, out_dtype)
+    Y = M.new_empty((*lead, c.m), dtype=dt)
+    rc = load().externd_ternary_apply_i8(
+        c.codes_B.data_ptr(), c.codes_C.data_ptr(), c.D.data_ptr(), c.bound.data_ptr(), c.m, c.n,
+        c.D.shape[0], M.data_ptr(), kind, ldx, s, M.shape[0], Y.data_ptr(), _TYPES[dt], c.m,
+        _raw_stream(device))
     if rc != OK:
         raise ExterndError(rc, "externd_ternary_apply_i8")
     return Y
