@@ -27,7 +27,14 @@ constexpr int64_t kPassRows = 4096;
 int64_t type_size(int type) { return type == EXTERND_F32 ? 4 : type == EXTERND_I8 ? 1 : 2; }
 
 int gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st) {
-  return a.rows > kTokens ? mma_gemm(a, epi, after_rows, st) : token_gemm(a, epi, after_rows, st);
+  if (a.rows <= kTokens) return token_gemm(a, epi, after_rows, st);
+  int dev = 0, nsm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EXTERND_ERR_CUDA;
+  cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+  SplitPlan p;
+  if (split_plan(a, epi, dev, &p) && p.cost < mma_cost(a, epi, nsm))
+    return split_gemm(a, p, epi, after_rows, st);
+  return mma_gemm(a, epi, after_rows, st);
 }
 
 // The device's status word (its address does not change; looking it up costs

@@ -23,6 +23,14 @@ constexpr int kTokens = 4;          // most rows of token_gemm
 constexpr int kTokenInner = 32768;  // longest token that token_raw quantises
 int token_raw(const GemmArgs& a, Epilogue epi, cudaStream_t st);
 int token_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
+struct SplitPlan {
+  int MT, TT, per, S;  // tiles of 128 weight rows, of `per` tokens, CTAs that split K
+  long long cost;      // estimated time, as mma_cost
+};
+bool split_plan(const GemmArgs& a, Epilogue epi, int dev, SplitPlan* p);
+int split_gemm(const GemmArgs& a, const SplitPlan& p, Epilogue epi, bool after_rows,
+               cudaStream_t st);
+long long mma_cost(const GemmArgs& a, Epilogue epi, int nsm);
 int mma_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
 int quantize(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8_t* Q, int64_t ldq,
              float* scale, cudaStream_t st);

@@ -1,0 +1,445 @@
+// 8-bit products whose tiles are too few to occupy the GPU (decoding batches,
+// short prompts, small matrices), on the tensor cores with the inner
+// dimension split over a thread-block cluster.
+//
+// A cluster of S <= 8 CTAs computes one tile of 128 weight rows x NT columns
+// (tokens, or the two planes of NT / 2 tokens), each CTA a run of the K steps:
+// the weights' bytes, which bound these products, stream through S times as
+// many SMs.  The CTAs leave their whole-number sums in shared memory, and each
+// adds and finishes its share of the tile through distributed shared memory.
+// Whole-number sums are exact, so the split does not show in the results.
+// The weights of the first ring fill are requested before the kernel waits
+// for the one in front of it.
+//
+// Warp roles: 0 TMA producer, 1 MMA issuer, 2 tensor-memory allocation, 4..11
+// unpack codes (two groups of four, alternate steps), then read the
+// accumulator out and finish.  Waits are bounded as in int8_mma.cu.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include "common.cuh"
+#include "int8.cuh"
+#include "int8_internal.h"
+#include "int8_umma.cuh"
+#include "internal.h"
+
+namespace externd {
+namespace i8 {
+namespace {
+
+constexpr int kMaxStages = 8, kMaxSplit = 8;
+constexpr int kSplitThreads = 384, kFinishWarp0 = 4, kFinishWarps = 8;
+constexpr int kSplitSmemMax = 222 * 1024;  // (the scales and barriers take the rest)
+// at least this much, so that no two CTAs of these kernels share an SM
+constexpr int kSplitSmemMin = 116 * 1024;
+
+struct SplitBars {
+  uint64_t full[kMaxStages], empty[kMaxStages], codes[kMaxStages], accf, drain;
+};
+
+__device__ __forceinline__ void tma_3d_own(uint32_t dst, const void* map, int x, int y, int z,
+                                           uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t in_peer(uint32_t addr, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ int4 peer_load(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void add4(int4& a, const int4& b) {
+  a.x += b.x;
+  a.y += b.y;
+  a.z += b.z;
+  a.w += b.w;
+}
+
+constexpr int kUnit = 2;  // tokens a warp finishes at a time
+
+// four values to four neighbours, in one store where they are aligned
+__device__ __forceinline__ void store4(float* y, const float (&v)[4], int n) {
+  if (n == 4 && ((uintptr_t)y & 15) == 0) {
+    *(float4*)y = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) y[e] = v[e];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* y, const float (&v)[4], int n) {
+  alignas(8) T h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) round_to(v[e], h[e]);
+  if (n == 4 && ((uintptr_t)y & 7) == 0) {
+    *(uint2*)y = *(const uint2*)h;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) y[e] = h[e];
+  }
+}
+
+// Four weight rows from i on and token t, from their whole sums.
+template <Epilogue EPI>
+__device__ __forceinline__ void finish_rows(const GemmArgs& a, const int4& v4, const int4& l4,
+                                            const float (&ws)[4], const float (&bias)[4], int i,
+                                            int t) {
+  const int v[4] = {v4.x, v4.y, v4.z, v4.w}, lo[4] = {l4.x, l4.y, l4.z, l4.w};
+  const int n = min(4, a.M - i);
+  if (n <= 0) return;
+  if (EPI == kOutPlanes) {
+    const float z = a.z[t];
+    const bool safe = safe_scale(z);
+    const float inv = safe ? __fdiv_rn(1.f, z) : 0.f, half = 0.5f * z;
+    uint32_t hi = 0u, low = 0u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float p = ws[e] * (float)(v[e] >> kCodeShift);
+      const uint32_t h =
+          128u + (safe ? settled(round_quotient(p, z, inv), half) : (uint32_t)component_value(p, z));
+      hi |= ((h >> 8) & 0xffu) << (8 * e);
+      low |= (h & 0xffu) << (8 * e);
+    }
+    // (rows past M fall into the padding of the token's row)
+    int8_t* y = (int8_t*)a.y + (int64_t)t * a.ldy + i;
+    *(uint32_t*)y = hi;
+    *(uint32_t*)(y + a.plane) = low ^ 0x80808080u;
+  } else {
+    const float s = a.xscale[t], z = EPI == kOutFactors ? a.z[t] : 0.f;
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (EPI == kOutDense) {
+        const float p = ws[e] * (float)v[e];
+        y[e] = a.bias ? fmaf(s, p, bias[e]) : s * p;
+      } else {
+        y[e] = s * (z * (0.015625f * fmaf(256.f, (float)v[e], (float)lo[e])));
+      }
+    }
+    const int64_t at = (int64_t)t * a.ldy + i;
+    if (a.ytype == EXTERND_BF16)
+      store4((__nv_bfloat16*)a.y + at, y, n);
+    else if (a.ytype == EXTERND_F16)
+      store4((__half*)a.y + at, y, n);
+    else
+      store4((float*)a.y + at, y, n);
+  }
+}
+
+template <bool CODES, Epilogue EPI>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+    split_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+                 const GemmArgs a, int NT, int S, int stages) {
+  constexpr int P = EPI == kOutFactors ? 2 : 1;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* ring = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  __shared__ __align__(8) SplitBars bars;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int rank = (int)cluster_rank();
+  const int i0 = (int)(blockIdx.x / S) * 128, per = NT / P, t0 = blockIdx.y * per;
+  const int ksteps = (a.K + kKStep - 1) / kKStep;
+  const int k0 = rank * ksteps / S, steps = (rank + 1) * ksteps / S - k0;
+  const int xbytes = NT * kKStep;
+  const int stage_bytes = kOperand + xbytes + (CODES ? kCodeBytes : 0);
+  const uint32_t tcols = NT <= 32 ? 32u : NT <= 64 ? 64u : NT <= 128 ? 128u : 256u;
+  volatile int* ab = &abort_flag;
+
+  if (wid == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tmem_base)),
+                 "r"(tcols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) {
+      bar_init(smem_u32(&bars.full[s]), CODES ? 5 : 1);
+      bar_init(smem_u32(&bars.empty[s]), 1);
+      bar_init(smem_u32(&bars.codes[s]), 1);
+    }
+    bar_init(smem_u32(&bars.accf), 1);
+    bar_init(smem_u32(&bars.drain), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    abort_flag = 0;
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_trigger();
+
+  if (wid == 0) {
+    if (elect_one()) {  // ---- TMA producer ----
+      auto weights = [&](int i) {
+        const int s = i % stages;
+        const uint32_t dst = smem_u32(ring + s * stage_bytes);
+        if (CODES) {
+          const uint32_t bar = smem_u32(&bars.codes[s]);
+          bar_expect(bar, kCodeBytes);
+          tma_2d_own(dst + kOperand + xbytes, &wmap, (k0 + i) * kCodeRow, i0, bar);
+        } else {
+          const uint32_t bar = smem_u32(&bars.full[s]);
+          bar_expect(bar, kOperand + xbytes);
+          tma_2d_own(dst, &wmap, (k0 + i) * kKStep, i0, bar);
+        }
+      };
+      auto tokens = [&](int i) {
+        const int s = i % stages;
+        const uint32_t bar = smem_u32(&bars.full[s]);
+        const uint32_t dst = smem_u32(ring + s * stage_bytes) + kOperand;
+        if (CODES) bar_expect(bar, xbytes);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          tma_3d_own(dst + p * per * kKStep, &xmap, (k0 + i) * kKStep, t0, p, bar);
+      };
+      const int ahead = min(stages, steps);
+      for (int i = 0; i < ahead; ++i) weights(i);
+      pdl_wait();
+      for (int i = 0; i < ahead; ++i) tokens(i);
+      for (int i = ahead; i < steps; ++i) {
+        const int s = i % stages;
+        if (!bar_wait(smem_u32(&bars.empty[s]), ((i / stages) + 1) & 1, ab, a.budget)) break;
+        weights(i);
+        tokens(i);
+      }
+    }
+  } else if (wid == 1) {
+    // ---- MMA issuer (the whole warp) ----
+    const uint32_t idesc = instr_desc(128, NT), base = smem_u32(ring);
+    const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
+    int s = 0, phase = 0;
+    bool ready = false;
+    for (int i = 0; i < steps; ++i) {
+      if (!warp_wait(ready, smem_u32(&bars.full[s]), phase, ab, a.budget)) break;
+      const uint32_t at = base + s * stage_bytes, done = smem_u32(&bars.empty[s]);
+      if (++s == stages) s = 0, phase ^= 1;
+      ready = bar_peek(smem_u32(&bars.full[s]), phase);  // (the next step's)
+      mma_step<false>(acc, operand_desc(at), operand_desc(at + kOperand), idesc, i > 0, done);
+    }
+    mma_commit<false>(smem_u32(&bars.accf));
+    mma_commit<false>(smem_u32(&bars.drain));
+    int never = 0;
+    bar_wait(smem_u32(&bars.drain), 0u, &never, kDefaultWaitBudget);
+  } else if (wid >= kFinishWarp0) {
+    const int quad = wid & 3, half = (wid - kFinishWarp0) >> 2;
+    if (CODES) {  // ---- codes: a row a thread, the two groups on alternate steps ----
+      const int row = quad * 32 + lane;
+      // (a stage's codes land after its last MMAs are done: the operand is free)
+      for (int i = half; i < steps; i += 2) {
+        const int s = i % stages;
+        const bool got = bar_wait(smem_u32(&bars.codes[s]), (i / stages) & 1, ab, a.budget);
+        if (!__all_sync(0xffffffffu, got)) break;
+        unsigned char* stage = ring + s * stage_bytes;
+        unpack_row(stage + kOperand + xbytes, stage, row);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_u32(&bars.full[s]));
+      }
+    }
+    // ---- the CTA's sums: [column][row] over the ring, which is done with ----
+    const bool got = bar_wait(smem_u32(&bars.accf), 0u, ab, a.budget);
+    if (__all_sync(0xffffffffu, got)) {
+      fence_after();
+      int* sums = (int*)ring + quad * 32 + lane;
+      for (int c = half * 16; c < NT; c += 32) {
+        int v[16];
+        acc_load(tmem + ((uint32_t)(quad * 32) << 16) + c, v);
+        acc_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sums[(c + e) * 128] = v[e];
+      }
+    }
+  }
+  // (after a timeout: copies in flight land within the delay)
+  if (*ab) {
+    const long long w0 = clock64();
+    while (clock64() - w0 < 2000000LL) {
+    }
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (wid >= kFinishWarp0) {
+    // ---- the CTA's share of the tile: a warp takes kUnit tokens of all 128
+    // rows at a time, a lane four neighbouring rows ----
+    pdl_wait();
+    const int r = 4 * lane, i = i0 + r;
+    float ws[4], bias[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      ws[e] = EPI != kOutFactors && i + e < a.M ? a.wscale[i + e] : 0.f;
+      bias[e] = EPI == kOutDense && a.bias && i + e < a.M ? a.bias[i + e] : 0.f;
+    }
+    const uint32_t sums = smem_u32(ring) + (uint32_t)r * 4u;
+    const int left = min(per, a.rows - t0);
+    for (int c = (rank * kFinishWarps + wid - kFinishWarp0) * kUnit; c < left;
+         c += S * kFinishWarps * kUnit) {
+      int4 v[kUnit], lo[kUnit];
+#pragma unroll
+      for (int e = 0; e < kUnit; ++e) v[e] = lo[e] = make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int s0 = 0; s0 < kMaxSplit; s0 += 4) {
+        // (every load of four peers on its way before the first is used)
+        int4 pv[4][kUnit], pl[4][kUnit];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          if (s0 + s >= S) continue;
+          const uint32_t from = in_peer(sums, s0 + s) + (uint32_t)c * 512u;
+#pragma unroll
+          for (int e = 0; e < kUnit; ++e) {
+            pv[s][e] = peer_load(from + e * 512);
+            if (P == 2) pl[s][e] = peer_load(from + (per + e) * 512);
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          if (s0 + s >= S) continue;
+#pragma unroll
+          for (int e = 0; e < kUnit; ++e) {
+            add4(v[e], pv[s][e]);
+            if (P == 2) add4(lo[e], pl[s][e]);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kUnit; ++e)
+        if (c + e < left) finish_rows<EPI>(a, v[e], lo[e], ws, bias, i, t0 + c + e);
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // (a CTA's sums stay until every peer has read them)
+  if (wid == 2) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tcols)
+                 : "memory");
+  }
+  if (tid == 0 && abort_flag) atomicCAS(a.status, 0, EXTERND_ERR_TIMEOUT);
+}
+
+template <bool CODES, Epilogue EPI>
+int launch(const GemmArgs& a, const SplitPlan& p, bool after_rows, cudaStream_t st) {
+  constexpr int P = EPI == kOutFactors ? 2 : 1;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EXTERND_ERR_CUDA;
+  static std::once_flag once[64];
+  static cudaError_t set[64];
+  std::call_once(once[dev], [&] {
+    set[dev] = cudaFuncSetAttribute(split_kernel<CODES, EPI>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmemMax);
+  });
+  if (set[dev] != cudaSuccess) return EXTERND_ERR_CUDA;
+  const int NT = p.per * P;
+  CUtensorMap xmap, wmap;
+  if (!byte_map(&xmap, a.x, a.K, a.rows, a.ldx, P, P == 2 ? a.plane : a.ldx, kKStep, p.per) ||
+      !(CODES ? byte_map(&wmap, a.w, 4 * a.ldw, a.M, 4 * a.ldw, 0, 0, kCodeRow, kHalfRows)
+              : byte_map(&wmap, a.w, a.K, a.M, a.ldw, 0, 0, kKStep, kHalfRows)))
+    return EXTERND_ERR_CUDA;
+  const int stage_bytes = kOperand + NT * kKStep + (CODES ? kCodeBytes : 0);
+  const int stages = std::min(kMaxStages, (kSplitSmemMax - 1024) / stage_bytes);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.MT * p.S), (unsigned)p.TT);
+  cfg.blockDim = dim3(kSplitThreads);
+  cfg.dynamicSmemBytes =
+      std::max(stages * stage_bytes + 1024, kSplitSmemMin);
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.S;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = after_rows ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, split_kernel<CODES, EPI>, xmap, wmap, a, NT, p.S, stages) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return EXTERND_ERR_CUDA;
+  }
+  return EXTERND_OK;
+}
+
+// Clusters of S CTAs, one CTA per SM, that the device holds at once.
+int resident_clusters(int dev, int S) {
+  static std::once_flag once[64];
+  static int held[64][kMaxSplit + 1];
+  std::call_once(once[dev], [&] {
+    cudaFuncSetAttribute(split_kernel<false, kOutDense>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         kSplitSmemMax);
+    for (int s = 1; s <= kMaxSplit; ++s) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)s);
+      cfg.blockDim = dim3(kSplitThreads);
+      cfg.dynamicSmemBytes = kSplitSmemMin;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = (unsigned)s;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, split_kernel<false, kOutDense>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+      }
+      held[dev][s] = n;
+    }
+  });
+  return held[dev][S];
+}
+
+}  // namespace
+
+// The largest split whose clusters the device holds at once; false where there
+// is none.
+bool split_plan(const GemmArgs& a, Epilogue epi, int dev, SplitPlan* p) {
+  const int P = epi == kOutFactors ? 2 : 1;
+  const int most = 256 / P, unit = 16 / P;
+  p->MT = (a.M + 127) / 128;
+  p->TT = (a.rows + most - 1) / most;
+  p->per = ((a.rows + p->TT - 1) / p->TT + unit - 1) / unit * unit;
+  const long long tiles = (long long)p->MT * p->TT;
+  const int ksteps = (a.K + kKStep - 1) / kKStep;
+  p->S = 0;
+  int least = 0;
+  for (int s = 1; s <= kMaxSplit && s <= ksteps; ++s) {
+    const int steps = (ksteps + s - 1) / s;
+    if (s > 1 && steps < 2) break;
+    if (tiles <= resident_clusters(dev, s) && (p->S == 0 || steps < least)) {
+      p->S = s;
+      least = steps;
+    }
+  }
+  // in units of 10 ns: a step of a narrow tile; the sums of S > 1 CTAs cross the
+  // cluster at some 10 bytes a cycle and CTA
+  p->cost = 600 + least * (16 + p->per * P / 16) + p->per * P * 3;
+  return p->S > 0;
+}
+
+int split_gemm(const GemmArgs& a, const SplitPlan& p, Epilogue epi, bool after_rows,
+               cudaStream_t st) {
+  if (epi == kOutDense) return launch<false, kOutDense>(a, p, after_rows, st);
+  if (epi == kOutPlanes) return launch<true, kOutPlanes>(a, p, after_rows, st);
+  return launch<true, kOutFactors>(a, p, after_rows, st);
+}
+
+}  // namespace i8
+}  // namespace externd

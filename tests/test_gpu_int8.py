@@ -152,9 +152,20 @@ def test_matmul_quantized(t, mn):
     R.check(y, *R.dense(x.q, x.scale, w.q, w.scale))
 
 
+@pytest.mark.parametrize("tmn", [(1100, 2001, 300), (3000, 1500, 129), (2048, 2560, 640),
+                                 (4100, 5000, 64), (40, 9729, 130), (5, 12000, 256),
+                                 (600, 20000, 48)])
+def test_matmul_many_tiles(tmn):
+    """More tiles than the GPU holds at once: whole and ragged ones."""
+    t, m, n = tmn
+    x, w = _held(t, n, t + m), _held(m, n, t + n)
+    bias = torch.randn(m, generator=_gen(4), device="cuda")
+    R.check(X.matmul_i8(x, w, bias=bias), *R.dense(x.q, x.scale, w.q, w.scale, bias))
+
+
 @pytest.mark.parametrize("xtype", FLOATS)
 @pytest.mark.parametrize("ytype", FLOATS)
-@pytest.mark.parametrize("t", [1, 20, 150])
+@pytest.mark.parametrize("t", [1, 20, 150, 2100])
 def test_matmul_types_and_bias(xtype, ytype, t):
     m, n = 270, 333
     x, w = _x(t, n, xtype, t), _held(m, n, 3)
@@ -167,7 +178,7 @@ def test_matmul_types_and_bias(xtype, ytype, t):
     assert X.matmul_i8(x, w).dtype == xtype
 
 
-@pytest.mark.parametrize("t", [1, 40, 300])
+@pytest.mark.parametrize("t", [1, 3, 40, 300, 20000])
 def test_matmul_largest_sums(t):
     """The longest inner dimension with every product at its largest: sums of
     both signs next to the ends of 32 bits."""
@@ -259,9 +270,20 @@ def test_apply(t, mnk):
     assert torch.equal(X.apply_i8(c, X.quantize_rows(x)), y)
 
 
+@pytest.mark.parametrize("tmnk", [(1500, 1300, 257, 2100), (2000, 2560, 128, 1111),
+                                  (4096, 300, 400, 5003), (40, 9730, 130, 129),
+                                  (700, 129, 1000, 9000)])
+def test_apply_many_tiles(tmnk):
+    t, m, n, k = tmnk
+    f, B, C, D = _factors(m, n, k, t + k)
+    x = _x(t, n, torch.float16, t)
+    y = X.apply_i8(X.pack_codes(f), x, out_dtype=torch.float32)
+    R.check(y, *R.factors(*R.rows(x), B, C, D))
+
+
 @pytest.mark.parametrize("xtype", FLOATS)
 @pytest.mark.parametrize("ytype", FLOATS)
-@pytest.mark.parametrize("t", [1, 40])
+@pytest.mark.parametrize("t", [1, 40, 2100])
 def test_apply_types(xtype, ytype, t):
     f, B, C, D = _factors(200, 150, 333, 3)
     x = _x(t, 150, xtype, t)
@@ -270,7 +292,7 @@ def test_apply_types(xtype, ytype, t):
     R.check(y, *R.factors(*R.rows(x), B, C, D))
 
 
-@pytest.mark.parametrize("t", [1, 70])
+@pytest.mark.parametrize("t", [1, 3, 70, 30000])
 def test_apply_extreme_factors(t):
     """Zero scales, empty components and rows, dense same-sign factors whose
     sums reach the bound, tiny and huge scales, D that is not finite."""
