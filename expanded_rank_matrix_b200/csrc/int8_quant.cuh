@@ -33,24 +33,35 @@ __device__ __forceinline__ void load_vec(const T* x, int j, int n, int G, T (&v)
   }
 }
 
-// Largest magnitude bits seen so far: the bit patterns of non-negative floats
-// order like integers in every type, and a NaN is above infinity.
+// Largest magnitude seen so far, as bits: those of one fp32, or of two 16-bit
+// values side by side.  A NaN stays (and is above infinity as bits).
 __device__ __forceinline__ uint32_t top_bits(uint32_t top, const float (&v)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
   return top;
 }
-template <typename T>  // 16-bit types: two magnitudes side by side
-__device__ __forceinline__ uint32_t top_bits(uint32_t top, const T (&v)[8]) {
+__device__ __forceinline__ uint32_t top_bits(uint32_t top, const __half (&v)[8]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) top = __vmaxu2(top, ((const uint32_t*)v)[e] & 0x7fff7fffu);
+  for (int e = 0; e < 4; ++e) {
+    const __half2 m = __hmax2_nan(*(const __half2*)&top, __habs2(((const __half2*)v)[e]));
+    top = *(const uint32_t*)&m;
+  }
+  return top;
+}
+__device__ __forceinline__ uint32_t top_bits(uint32_t top, const __nv_bfloat16 (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 m =
+        __hmax2_nan(*(const __nv_bfloat162*)&top, __habs2(((const __nv_bfloat162*)v)[e]));
+    top = *(const uint32_t*)&m;
+  }
   return top;
 }
 // the magnitude those bits stand for (as fp32 bits)
 __device__ __forceinline__ uint32_t top_value(uint32_t top, float) { return top; }
 template <typename T>
 __device__ __forceinline__ uint32_t top_value(uint32_t top, T) {
-  const uint16_t u = (uint16_t)max(top & 0xffffu, top >> 16);
+  const uint16_t u = (uint16_t)max(top & 0x7fffu, (top >> 16) & 0x7fffu);
   T h;
   *(uint16_t*)&h = u;
   return __float_as_uint(to_f32(h)) & 0x7fffffffu;
@@ -75,27 +86,37 @@ __device__ __forceinline__ float row_scale(uint32_t top) {
   return top < 0x7f800000u ? __fdiv_rn(__uint_as_float(top), 127.f) : __uint_as_float(0x7fc00000u);
 }
 
-// 8-bit values of E elements, in the low byte of each word.
+// 8-bit values of E elements, in the low byte of each word: x / s to the nearest
+// whole number, ties to even, exactly.  1 / s lies between inv (1 - 2^-22) and
+// inv (1 + 2^-22), so the quotient lies between the two products; rounding is
+// monotone, so where both round to one number (by the constant kRound, one
+// fused operation each) that is the quotient's.  The few vectors where some
+// pair differs are settled by their remainders.
 template <typename T, int E>
 __device__ __forceinline__ void quantize_vec(const T (&u)[E], float s, float inv, bool safe,
                                              uint32_t (&b)[E]) {
-  const float half = 0.5f * s;
-  Rounded r[E];
-  float far = 0.f;
+  const float above = inv * (1.f + 0x1p-22f), below = inv * (1.f - 0x1p-22f);
+  const F2 above2 = f2(above, above), below2 = f2(below, below), round2 = f2(kRound, kRound);
+  uint32_t differ = 0u;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    r[e] = round_quotient(to_f32(u[e]), s, inv);
-    b[e] = low_bits(r[e]);
-    far = fmaxf(far, fabsf(r[e].remainder));
+  for (int e = 0; e < E; e += 2) {
+    const F2 x2 = f2(to_f32(u[e]), to_f32(u[e + 1]));
+    float y0, y1, z0, z1;
+    split(fma2(x2, above2, round2), y0, y1);
+    split(fma2(x2, below2, round2), z0, z1);
+    b[e] = __float_as_uint(y0);
+    b[e + 1] = __float_as_uint(y1);
+    differ |= b[e] ^ __float_as_uint(z0);
+    differ |= b[e + 1] ^ __float_as_uint(z1);
   }
   if (!safe) {
 #pragma unroll
     for (int e = 0; e < E; ++e)
       // (a subnormal scale may put x / s past 127: the clamp keeps 8 bits)
       b[e] = s > 0.f ? (uint32_t)max(-127, min(127, nearest_quotient(to_f32(u[e]), s))) : 0u;
-  } else if (far >= half) {
+  } else if (differ) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) b[e] = settled(r[e], half);
+    for (int e = 0; e < E; ++e) b[e] = settled(round_quotient(to_f32(u[e]), s, inv), 0.5f * s);
   }
 }
 

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rows_kernel(cons
 #pragma unroll
     for (int p = 0; p < E / 4; ++p) {
       packed[p] = pack_bytes(b[4 * p], b[4 * p + 1], b[4 * p + 2], b[4 * p + 3]);
-      squares = __dp4a((int)packed[p], (int)packed[p], (int)squares);
+      if (a.z) squares = __dp4a((int)packed[p], (int)packed[p], (int)squares);
     }
     if (VEC && j + E <= a.n) {
       if (E == 8)

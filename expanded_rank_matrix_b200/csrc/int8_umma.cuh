@@ -238,27 +238,6 @@ __device__ __forceinline__ void store_column(T* y, int64_t ldy, int left, const 
   }
 }
 
-// Two fp32 values side by side (packed arithmetic, IEEE per value).
-typedef unsigned long long F2;
-__device__ __forceinline__ F2 f2(float x, float y) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void split(F2 v, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // Component values of one weight row (D / 64 = ws) and N tokens: h + 128 in
 // the low 16 bits of each word (round_quotient with 128 more in its constant,
 // so that byte 1 is plane hi and byte 0, less 128, plane lo).

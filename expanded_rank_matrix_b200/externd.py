@@ -354,8 +354,13 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 def _matrix(X: torch.Tensor):
     """(matrix of X's rows, distance between rows): X [..., n] itself where its
     rows lie at one distance and their elements side by side, else a copy."""
-    M = X if X.dim() == 2 else X.reshape(-1, X.shape[-1])
-    rows, n = M.shape
+    n = X.shape[-1]
+    if n == 0:
+        raise ValueError("expected at least one column")
+    if X.is_contiguous():
+        return X if X.dim() == 2 else X.view(-1, n), n
+    M = X if X.dim() == 2 else X.reshape(-1, n)
+    rows = M.shape[0]
     if (n > 1 and M.stride(1) != 1) or (rows > 1 and M.stride(0) < n):
         M = M.contiguous()
     # (the stride of a single row means nothing)
@@ -412,7 +417,7 @@ def quantize_rows(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -
     M, ldx = _matrix(X)
     rows, n = M.shape
     ldq = (n + 15) // 16 * 16
-    q = M.new_empty((rows, ldq), dtype=torch.int8)
+    q = M.new_empty(rows, ldq, dtype=torch.int8)
     scale = M.new_empty(rows, dtype=torch.float32)
     rc = load().externd_quantize_rows(M.data_ptr(), kind, ldx, rows, n, q.data_ptr(), ldq,
                                       scale.data_ptr(), _raw_stream(device))
@@ -425,7 +430,7 @@ def quantize_rows(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -
 
 def _activations(X, n: int, device: int, out_dtype):
     """(matrix, its scales' address, type, row distance, leading sizes, output
-    type) of the activations of an 8-bit product."""
+    type and its number) of the activations of an 8-bit product."""
     if X.__class__ is Quantized:
         M, s, kind, ldx, lead = X.q, X.scale.data_ptr(), I8, X._ld, X.q.shape[:1]
         where, dt = X._device, out_dtype or torch.float32
@@ -440,9 +445,10 @@ def _activations(X, n: int, device: int, out_dtype):
         raise ValueError("expected tensors on one CUDA device")
     if M.shape[1] != n:
         raise ValueError(f"X must have {n} columns")
-    if dt not in _TYPES:
+    out = _TYPES.get(dt)
+    if out is None:
         raise ValueError("out_dtype must be fp32, fp16 or bf16")
-    return M, s, kind, ldx, lead, dt
+    return M, s, kind, ldx, lead, dt, out
 
 
 def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=None,
@@ -457,17 +463,17 @@ def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=No
         with _on(device, stream):
             return matmul_i8(X, W, bias, out_dtype)
     m, n = W.q.shape
-    M, s, kind, ldx, lead, dt = _activations(X, n, device, out_dtype)
+    M, s, kind, ldx, lead, dt, out = _activations(X, n, device, out_dtype)
     b = None
     if bias is not None:
         bias = _vector(bias, m, "bias")
         if bias.get_device() != device:
             raise ValueError("expected tensors on one CUDA device")
         b = bias.data_ptr()
-    Y = M.new_empty((*lead, m), dtype=dt)
+    Y = M.new_empty(*lead, m, dtype=dt)
     rc = load().externd_matmul_i8(M.data_ptr(), kind, ldx, s, W.q.data_ptr(), W._ld,
                                   W.scale.data_ptr(), b, M.shape[0], n, m, Y.data_ptr(),
-                                  _TYPES[dt], m, _raw_stream(device))
+                                  out, m, _raw_stream(device))
     if rc != OK:
         raise ExterndError(rc, "externd_matmul_i8")
     return Y
@@ -536,11 +542,11 @@ def apply_i8(c: FactorCodes, X, out_dtype=None,
     if _elsewhere(device, stream):
         with _on(device, stream):
             return apply_i8(c, X, out_dtype)
-    M, s, kind, ldx, lead, dt = _activations(X, c.n, device, out_dtype)
-    Y = M.new_empty((*lead, c.m), dtype=dt)
+    M, s, kind, ldx, lead, dt, out = _activations(X, c.n, device, out_dtype)
+    Y = M.new_empty(*lead, c.m, dtype=dt)
     rc = load().externd_ternary_apply_i8(
         c.codes_B.data_ptr(), c.codes_C.data_ptr(), c.D.data_ptr(), c.bound.data_ptr(), c.m, c.n,
-        c.D.shape[0], M.data_ptr(), kind, ldx, s, M.shape[0], Y.data_ptr(), _TYPES[dt], c.m,
+        c.D.shape[0], M.data_ptr(), kind, ldx, s, M.shape[0], Y.data_ptr(), out, c.m,
         _raw_stream(device))
     if rc != OK:
         raise ExterndError(rc, "externd_ternary_apply_i8")
