@@ -90,11 +90,14 @@ __device__ __forceinline__ float row_scale(uint32_t top) {
 // whole number, ties to even, exactly.  1 / s lies between inv (1 - 2^-22) and
 // inv (1 + 2^-22), so the quotient lies between the two products; rounding is
 // monotone, so where both round to one number (by the constant kRound, one
-// fused operation each) that is the quotient's.  The few vectors where some
-// pair differs are settled by their remainders.
-template <typename T, int E>
-__device__ __forceinline__ void quantize_vec(const T (&u)[E], float s, float inv, bool safe,
-                                             uint32_t (&b)[E]) {
+// fused operation each) that is the quotient's.  Vectors where some pair
+// differs are few; SETTLE settles them here by their remainders, else other
+// than 0 is returned and settle_row has to.  (Here costs code, which tells in a
+// kernel of a few microseconds; there a second read of the vector, which
+// tells in a long one: 8192 x 2560 bf16 rows take 13.8 us this way, 15.8 that.)
+template <bool SETTLE, typename T, int E>
+__device__ __forceinline__ uint32_t quantize_vec(const T (&u)[E], float s, float inv,
+                                                 uint32_t (&b)[E]) {
   const float above = inv * (1.f + 0x1p-22f), below = inv * (1.f - 0x1p-22f);
   const F2 above2 = f2(above, above), below2 = f2(below, below), round2 = f2(kRound, kRound);
   uint32_t differ = 0u;
@@ -109,15 +112,49 @@ __device__ __forceinline__ void quantize_vec(const T (&u)[E], float s, float inv
     differ |= b[e] ^ __float_as_uint(z0);
     differ |= b[e + 1] ^ __float_as_uint(z1);
   }
-  if (!safe) {
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      // (a subnormal scale may put x / s past 127: the clamp keeps 8 bits)
-      b[e] = s > 0.f ? (uint32_t)max(-127, min(127, nearest_quotient(to_f32(u[e]), s))) : 0u;
-  } else if (differ) {
+  if (SETTLE && differ) {
 #pragma unroll
     for (int e = 0; e < E; ++e) b[e] = settled(round_quotient(to_f32(u[e]), s, inv), 0.5f * s);
+    differ = 0u;
   }
+  return differ;
+}
+
+// The exact values of a thread's elements of a row once more, where quantize_vec
+// was not sure of a vector (bit h of `which` for the thread's h-th one, the
+// last bit for all from there on), or of all where the scale is not safe.  q:
+// the row's bytes, in global or shared memory.  Returns what the sum of
+// squares changes by.  Out of line: it is rare, and its code would crowd the
+// instruction cache of the short kernels.
+template <typename T, bool VEC>
+__device__ __noinline__ int settle_row(const T* x, int n, int tid, int G, float s, float inv,
+                                       uint32_t which, int8_t* q) {
+  constexpr int E = 16 / sizeof(T);
+  const bool safe = safe_scale(s);
+  const int step = VEC ? 1 : G;
+  int change = 0;
+#pragma unroll 1
+  for (int h = 0; first_of<T, VEC>(h, 0, G) < n; ++h) {
+    if (safe && !((which >> min(h, 31)) & 1u)) continue;
+    const int j = first_of<T, VEC>(h, tid, G);
+    T u[E];
+    load_vec<T, VEC>(x, j, n, G, u);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (j + e * step >= n) continue;
+      const float v = to_f32(u[e]);
+      const int was = q[j + e * step];
+      int is = 0;
+      if (safe)
+        is = (int8_t)settled(round_quotient(v, s, inv), 0.5f * s);
+      else if (s > 0.f)
+        // (a subnormal scale may put x / s past 127: the clamp keeps 8 bits)
+        is = max(-127, min(127, nearest_quotient(v, s)));
+      q[j + e * step] = (int8_t)is;
+      change += is * is - was * was;
+    }
+  }
+  return change;
 }
 
 // four of those words as four bytes

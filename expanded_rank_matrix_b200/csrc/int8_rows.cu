@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rows_kernel(cons
   uint32_t squares = 0u;
   auto emit = [&](int j, const T (&u)[E]) {
     uint32_t b[E];
-    quantize_vec(u, s, inv, safe, b);
+    quantize_vec<true>(u, s, inv, b);
     uint32_t packed[E / 4];
 #pragma unroll
     for (int p = 0; p < E / 4; ++p) {
@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rows_kernel(cons
     load_vec<T, VEC>(x, j, a.n, G, u);
     emit(j, u);
   }
+  if (!safe) squares += (uint32_t)settle_row<T, VEC>(x, a.n, tid, G, s, inv, 0u, q);
   if (a.z) {
     squares = group_reduce<WARP, false>(squares, red[1]);
     if (tid == 0)

@@ -58,14 +58,14 @@ __device__ __forceinline__ float quantize_token(const T* x, int n, int padded, u
   const float s = row_scale(top);
   const bool safe = safe_scale(s);
   const float inv = safe ? __fdiv_rn(1.f, s) : 0.f;
-  uint32_t sq = 0u;
+  uint32_t sq = 0u, which = 0u;
 #pragma unroll 2
   for (int h = 0; h * G * E < padded; ++h) {
     const int j = first_of<T, VEC>(h, tid, G);
     T u[E];
     uint32_t b[E];
     load_vec<T, VEC>(x, j, n, G, u);  // (zeros past n: value 0)
-    quantize_vec(u, s, inv, safe, b);
+    if (quantize_vec<false>(u, s, inv, b)) which |= 1u << min(h, 31);
 #pragma unroll
     for (int p = 0; p < E / 4; ++p) {
       const uint32_t w = pack_bytes(b[4 * p], b[4 * p + 1], b[4 * p + 2], b[4 * p + 3]);
@@ -79,6 +79,8 @@ __device__ __forceinline__ float quantize_token(const T* x, int n, int padded, u
       }
     }
   }
+  if (which || !safe)
+    sq += (uint32_t)settle_row<T, VEC>(x, n, tid, G, s, inv, which, (int8_t*)xs);
   if (want) *squares = group_reduce<false, false>(sq, red + 32);
   return s;
 }

@@ -333,11 +333,6 @@ def _device_of(t: torch.Tensor, *others) -> int:
     return index
 
 
-def _elsewhere(index: int, stream: Optional[torch.cuda.Stream]) -> bool:
-    """Whether a call has to change the current device or stream first (_on)."""
-    return stream is not None or index != torch._C._cuda_getDevice()
-
-
 def _on(index: int, stream: Optional[torch.cuda.Stream]):
     """Context in which the tensors' device, and a given stream, are current:
     what is allocated or copied inside belongs to the stream of the launch."""
@@ -349,6 +344,7 @@ def _on(index: int, stream: Optional[torch.cuda.Stream]):
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _matrix(X: torch.Tensor):
@@ -400,7 +396,9 @@ class Quantized:
 
     def _set(self, q, scale, ld, device):
         d = self.__dict__
-        d["q"], d["scale"], d["_ld"], d["_device"] = q, scale, ld, device
+        d["q"], d["scale"], d["_device"] = q, scale, device
+        # what every call passes on: address, row distance, the scales' address
+        d["_raw"] = q.data_ptr(), ld, scale.data_ptr()
 
 
 def quantize_rows(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> Quantized:
@@ -411,7 +409,7 @@ def quantize_rows(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -
     if kind is None or X.dim() == 0:
         raise ValueError("X must be an fp32, fp16 or bf16 tensor of at least one dimension")
     device = _device_of(X)
-    if _elsewhere(device, stream):
+    if stream is not None or device != _current_device():
         with _on(device, stream):
             return quantize_rows(X)
     M, ldx = _matrix(X)
@@ -429,26 +427,29 @@ def quantize_rows(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -
 
 
 def _activations(X, n: int, device: int, out_dtype):
-    """(matrix, its scales' address, type, row distance, leading sizes, output
-    type and its number) of the activations of an 8-bit product."""
+    """(the activations' address, type, row distance, scales' address, rows, the
+    output's number of type, and the output's leading sizes and a tensor to
+    allocate it from, and its type) for an 8-bit product."""
     if X.__class__ is Quantized:
-        M, s, kind, ldx, lead = X.q, X.scale.data_ptr(), I8, X._ld, X.q.shape[:1]
-        where, dt = X._device, out_dtype or torch.float32
+        M, kind, where, dt = X.q, I8, X._device, out_dtype or torch.float32
+        lead = (M.shape[0],)
+        at, ldx, s = X._raw
     else:
         kind = _TYPES.get(X.dtype)
         if kind is None or X.dim() == 0:
             raise ValueError("X must be Quantized, or an fp32, fp16 or bf16 tensor of at least "
                              "one dimension")
         (M, ldx), s, lead = _matrix(X), None, X.shape[:-1]
-        where, dt = X.get_device(), out_dtype or X.dtype
+        at, where, dt = M.data_ptr(), X.get_device(), out_dtype or X.dtype
+    rows, cols = M.shape
     if where != device:
         raise ValueError("expected tensors on one CUDA device")
-    if M.shape[1] != n:
+    if cols != n:
         raise ValueError(f"X must have {n} columns")
     out = _TYPES.get(dt)
     if out is None:
         raise ValueError("out_dtype must be fp32, fp16 or bf16")
-    return M, s, kind, ldx, lead, dt, out
+    return at, kind, ldx, s, rows, out, lead, M, dt
 
 
 def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=None,
@@ -459,11 +460,11 @@ def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=No
     several products).  The output is [..., m] of out_dtype (default: X's
     type; fp32 for Quantized)."""
     device = W._device
-    if _elsewhere(device, stream):
+    if stream is not None or device != _current_device():
         with _on(device, stream):
             return matmul_i8(X, W, bias, out_dtype)
     m, n = W.q.shape
-    M, s, kind, ldx, lead, dt, out = _activations(X, n, device, out_dtype)
+    at, kind, ldx, s, rows, out, lead, M, dt = _activations(X, n, device, out_dtype)
     b = None
     if bias is not None:
         bias = _vector(bias, m, "bias")
@@ -471,9 +472,9 @@ def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=No
             raise ValueError("expected tensors on one CUDA device")
         b = bias.data_ptr()
     Y = M.new_empty(*lead, m, dtype=dt)
-    rc = load().externd_matmul_i8(M.data_ptr(), kind, ldx, s, W.q.data_ptr(), W._ld,
-                                  W.scale.data_ptr(), b, M.shape[0], n, m, Y.data_ptr(),
-                                  out, m, _raw_stream(device))
+    w, ldw, ws = W._raw
+    rc = load().externd_matmul_i8(at, kind, ldx, s, w, ldw, ws, b, rows, n, m, Y.data_ptr(), out, m,
+                                  _raw_stream(device))
     if rc != OK:
         raise ExterndError(rc, "externd_matmul_i8")
     return Y
@@ -507,14 +508,17 @@ class FactorCodes:
                                (self.D, (k,), torch.float32), (self.bound, (1,), torch.float32)):
             if t.dtype != kind or t.shape != shape or not t.is_contiguous():
                 raise ValueError("codes, D and bound must be as pack_codes returns them")
-        self.__dict__["_device"] = _device_of(self.D, self.codes_B, self.codes_C, self.bound)
+        tensors = self.codes_B, self.codes_C, self.D, self.bound
+        self.__dict__["_device"] = _device_of(*tensors)
+        # what every call passes on
+        self.__dict__["_raw"] = (*(t.data_ptr() for t in tensors), self.m, self.n, k)
 
 
 def pack_codes(f: Factors, stream: Optional[torch.cuda.Stream] = None) -> FactorCodes:
     """Lays factors out once for apply_i8 (externd_pack_codes): those of a
     decomposition, or its first components (truncate)."""
     device = _device_of(f.D, f.packed_B, f.packed_C)
-    if _elsewhere(device, stream):
+    if stream is not None or device != _current_device():
         with _on(device, stream):
             return pack_codes(f)
     k = f.k
@@ -539,15 +543,13 @@ def apply_i8(c: FactorCodes, X, out_dtype=None,
     """X (B diag(D) C)^T on 8-bit activations, from the packed codes
     (externd_ternary_apply_i8).  X and out_dtype as for matmul_i8."""
     device = c._device
-    if _elsewhere(device, stream):
+    if stream is not None or device != _current_device():
         with _on(device, stream):
             return apply_i8(c, X, out_dtype)
-    M, s, kind, ldx, lead, dt, out = _activations(X, c.n, device, out_dtype)
+    at, kind, ldx, s, rows, out, lead, M, dt = _activations(X, c.n, device, out_dtype)
     Y = M.new_empty(*lead, c.m, dtype=dt)
-    rc = load().externd_ternary_apply_i8(
-        c.codes_B.data_ptr(), c.codes_C.data_ptr(), c.D.data_ptr(), c.bound.data_ptr(), c.m, c.n,
-        c.D.shape[0], M.data_ptr(), kind, ldx, s, M.shape[0], Y.data_ptr(), out, c.m,
-        _raw_stream(device))
+    rc = load().externd_ternary_apply_i8(*c._raw, at, kind, ldx, s, rows, Y.data_ptr(), out, c.m,
+                                         _raw_stream(device))
     if rc != OK:
         raise ExterndError(rc, "externd_ternary_apply_i8")
     return Y
