@@ -5,9 +5,13 @@
 // A cluster of S <= 8 CTAs computes one tile of 128 weight rows x NT columns
 // (tokens, or the two planes of NT / 2 tokens), each CTA a run of the K steps:
 // the weights' bytes, which bound these products, stream through S times as
-// many SMs.  The CTAs leave their whole-number sums in shared memory, and each
-// adds and finishes its share of the tile through distributed shared memory.
-// Whole-number sums are exact, so the split does not show in the results.
+// many SMs.  Every token of the tile has an owner among the CTAs, and each CTA
+// adds its whole-number sums of the token into the owner's shared memory by
+// asynchronous remote additions that count on the owner's barrier; when all
+// have come, the owner finishes its tokens.  Nothing waits on a round trip, and
+// no cluster barrier stands in the way.  (Peers reading one another's sums
+// between two cluster barriers took 3.5 us of an 8.4 us product.)  Whole-number
+// sums are exact in any order, so the split does not show in the results.
 // The weights of the first ring fill are requested before the kernel waits
 // for the one in front of it.
 //
@@ -39,7 +43,7 @@ constexpr int kSplitSmemMax = 222 * 1024;  // (the scales and barriers take the 
 constexpr int kSplitSmemMin = 116 * 1024;
 
 struct SplitBars {
-  uint64_t full[kMaxStages], empty[kMaxStages], codes[kMaxStages], accf, drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], codes[kMaxStages], accf, sums, drain;
 };
 
 __device__ __forceinline__ void tma_3d_own(uint32_t dst, const void* map, int x, int y, int z,
@@ -55,22 +59,14 @@ __device__ __forceinline__ uint32_t in_peer(uint32_t addr, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ int4 peer_load(uint32_t addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+// adds to a word of a CTA's shared memory; 4 bytes count on its barrier
+__device__ __forceinline__ void remote_add(uint32_t at, int v, uint32_t bar) {
+  asm volatile(
+      "red.async.relaxed.cluster.shared::cluster.mbarrier::complete_tx::bytes.add.s32 [%0], %1, "
+      "[%2];" ::"r"(at),
+      "r"(v), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ void add4(int4& a, const int4& b) {
-  a.x += b.x;
-  a.y += b.y;
-  a.z += b.z;
-  a.w += b.w;
-}
-
-constexpr int kUnit = 2;  // tokens a warp finishes at a time
 
 // four values to four neighbours, in one store where they are aligned
 __device__ __forceinline__ void store4(float* y, const float (&v)[4], int n) {
@@ -99,13 +95,12 @@ __device__ __forceinline__ void store4(T* y, const float (&v)[4], int n) {
 // Four weight rows from i on and token t, from their whole sums.
 template <Epilogue EPI>
 __device__ __forceinline__ void finish_rows(const GemmArgs& a, const int4& v4, const int4& l4,
-                                            const float (&ws)[4], const float (&bias)[4], int i,
-                                            int t) {
+                                            const float (&ws)[4], const float (&bias)[4], float s,
+                                            float z, int i, int t) {
   const int v[4] = {v4.x, v4.y, v4.z, v4.w}, lo[4] = {l4.x, l4.y, l4.z, l4.w};
   const int n = min(4, a.M - i);
   if (n <= 0) return;
   if (EPI == kOutPlanes) {
-    const float z = a.z[t];
     const bool safe = safe_scale(z);
     const float inv = safe ? __fdiv_rn(1.f, z) : 0.f, half = 0.5f * z;
     uint32_t hi = 0u, low = 0u;
@@ -122,7 +117,6 @@ __device__ __forceinline__ void finish_rows(const GemmArgs& a, const int4& v4, c
     *(uint32_t*)y = hi;
     *(uint32_t*)(y + a.plane) = low ^ 0x80808080u;
   } else {
-    const float s = a.xscale[t], z = EPI == kOutFactors ? a.z[t] : 0.f;
     float y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -150,6 +144,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   constexpr int P = EPI == kOutFactors ? 2 : 1;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  int* sums = (int*)(ring + stages * (kOperand + NT * kKStep + (CODES ? kCodeBytes : 0)));
   __shared__ __align__(8) SplitBars bars;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
@@ -162,6 +157,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const int stage_bytes = kOperand + xbytes + (CODES ? kCodeBytes : 0);
   const uint32_t tcols = NT <= 32 ? 32u : NT <= 64 ? 64u : NT <= 128 ? 128u : 256u;
   volatile int* ab = &abort_flag;
+  // the CTA's tokens: every S-th of the tile's, [token][plane][row] in `sums`
+  const int left = min(per, a.rows - t0), mine = max(0, (left - rank + S - 1) / S);
 
   if (wid == 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -170,7 +167,22 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (tid == 0) {
+  const bool producer = wid == 0 && elect_one();
+  const int ahead = min(stages, steps);
+  auto weights = [&](int i) {
+    const int s = i % stages;
+    const uint32_t dst = smem_u32(ring + s * stage_bytes);
+    if (CODES) {
+      const uint32_t bar = smem_u32(&bars.codes[s]);
+      bar_expect(bar, kCodeBytes);
+      tma_2d_own(dst + kOperand + xbytes, &wmap, (k0 + i) * kCodeRow, i0, bar);
+    } else {
+      const uint32_t bar = smem_u32(&bars.full[s]);
+      bar_expect(bar, kOperand + xbytes);
+      tma_2d_own(dst, &wmap, (k0 + i) * kKStep, i0, bar);
+    }
+  };
+  if (producer) {
     for (int s = 0; s < stages; ++s) {
       bar_init(smem_u32(&bars.full[s]), CODES ? 5 : 1);
       bar_init(smem_u32(&bars.empty[s]), 1);
@@ -178,30 +190,33 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     }
     bar_init(smem_u32(&bars.accf), 1);
     bar_init(smem_u32(&bars.drain), 1);
+    bar_init(smem_u32(&bars.sums), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    bar_expect(smem_u32(&bars.sums), (uint32_t)(mine * P * S * 512));
     abort_flag = 0;
+    // the weights of the first ring fill, before anything else
+    asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&xmap) : "memory");
+    for (int i = 0; i < ahead; ++i) weights(i);
   }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_base;
+  // the cluster's first barrier: every CTA's sums are zero and its barrier
+  // counts.  Only the warps that write the zeros publish anything, which takes
+  // them a thousand cycles that the others do not wait for.
+  if (wid >= kFinishWarp0) {
+    for (int e = tid - 32 * kFinishWarp0; e < mine * P * 32; e += 32 * kFinishWarps)
+      ((int4*)sums)[e] = make_int4(0, 0, 0, 0);
+    __syncwarp();
+    cluster_arrive();
+  } else {
+    cluster_arrive_relaxed();
+  }
   pdl_trigger();
 
   if (wid == 0) {
-    if (elect_one()) {  // ---- TMA producer ----
-      auto weights = [&](int i) {
-        const int s = i % stages;
-        const uint32_t dst = smem_u32(ring + s * stage_bytes);
-        if (CODES) {
-          const uint32_t bar = smem_u32(&bars.codes[s]);
-          bar_expect(bar, kCodeBytes);
-          tma_2d_own(dst + kOperand + xbytes, &wmap, (k0 + i) * kCodeRow, i0, bar);
-        } else {
-          const uint32_t bar = smem_u32(&bars.full[s]);
-          bar_expect(bar, kOperand + xbytes);
-          tma_2d_own(dst, &wmap, (k0 + i) * kKStep, i0, bar);
-        }
-      };
+    if (producer) {  // ---- TMA producer ----
       auto tokens = [&](int i) {
         const int s = i % stages;
         const uint32_t bar = smem_u32(&bars.full[s]);
@@ -211,8 +226,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         for (int p = 0; p < P; ++p)
           tma_3d_own(dst + p * per * kKStep, &xmap, (k0 + i) * kKStep, t0, p, bar);
       };
-      const int ahead = min(stages, steps);
-      for (int i = 0; i < ahead; ++i) weights(i);
       pdl_wait();
       for (int i = 0; i < ahead; ++i) tokens(i);
       for (int i = ahead; i < steps; ++i) {
@@ -255,17 +268,63 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         if (lane == 0) bar_arrive(smem_u32(&bars.full[s]));
       }
     }
-    // ---- the CTA's sums: [column][row] over the ring, which is done with ----
-    const bool got = bar_wait(smem_u32(&bars.accf), 0u, ab, a.budget);
-    if (__all_sync(0xffffffffu, got)) {
+    // ---- the CTA's sums to the tokens' owners ----
+    bool got = bar_wait(smem_u32(&bars.accf), 0u, ab, a.budget);
+    got = __all_sync(0xffffffffu, got);
+    __syncwarp();
+    cluster_wait();
+    if (got) {
       fence_after();
-      int* sums = (int*)ring + quad * 32 + lane;
+      const uint32_t at = smem_u32(sums) + (uint32_t)(quad * 32 + lane) * 4u;
+      const uint32_t bar = smem_u32(&bars.sums);
       for (int c = half * 16; c < NT; c += 32) {
         int v[16];
         acc_load(tmem + ((uint32_t)(quad * 32) << 16) + c, v);
         acc_wait();
+        // (per is a multiple of 8: a run of 8 columns lies in one plane)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sums[(c + e) * 128] = v[e];
+        for (int h = 0; h < 2; ++h) {
+          const int p = P == 2 && c + 8 * h >= per ? 1 : 0, u = c + 8 * h - p * per;
+          int slot = u / S, owner = u - slot * S;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (u + e < left)
+              remote_add(in_peer(at + (uint32_t)(slot * P + p) * 512u, owner), v[8 * h + e],
+                         in_peer(bar, owner));
+            if (++owner == S) owner = 0, ++slot;
+          }
+        }
+      }
+    }
+    // ---- the CTA's own tokens: a warp each, a lane four neighbouring rows ----
+    const int r = 4 * lane, i = i0 + r;
+    float ws[4], bias[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      ws[e] = EPI != kOutFactors && i + e < a.M ? a.wscale[i + e] : 0.f;
+      bias[e] = EPI == kOutDense && a.bias && i + e < a.M ? a.bias[i + e] : 0.f;
+    }
+    pdl_wait();
+    int j = wid - kFinishWarp0;
+    float s = 0.f, z = 0.f;
+    if (j < mine) {
+      if (EPI != kOutPlanes) s = a.xscale[t0 + j * S + rank];
+      if (EPI != kOutDense) z = a.z[t0 + j * S + rank];
+    }
+    got = bar_wait(smem_u32(&bars.sums), 0u, ab, a.budget);
+    got = __all_sync(0xffffffffu, got);
+    __syncwarp();
+    cluster_arrive_relaxed();
+    if (got) {
+      for (; j < mine; j += kFinishWarps) {
+        const int4 v = *(const int4*)(sums + j * P * 128 + r);
+        const int4 lo = P == 2 ? *(const int4*)(sums + (j * P + 1) * 128 + r) : make_int4(0, 0, 0, 0);
+        finish_rows<EPI>(a, v, lo, ws, bias, s, z, i, t0 + j * S + rank);
+        const int next = j + kFinishWarps;
+        if (next < mine) {
+          if (EPI != kOutPlanes) s = a.xscale[t0 + next * S + rank];
+          if (EPI != kOutDense) z = a.z[t0 + next * S + rank];
+        }
       }
     }
   }
@@ -275,58 +334,14 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     while (clock64() - w0 < 2000000LL) {
     }
   }
+  __syncwarp();
+  if (wid < kFinishWarp0) {
+    cluster_wait();
+    cluster_arrive_relaxed();
+  }
   fence_before();
   __syncthreads();
-  cluster_sync();
-  if (wid >= kFinishWarp0) {
-    // ---- the CTA's share of the tile: a warp takes kUnit tokens of all 128
-    // rows at a time, a lane four neighbouring rows ----
-    pdl_wait();
-    const int r = 4 * lane, i = i0 + r;
-    float ws[4], bias[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      ws[e] = EPI != kOutFactors && i + e < a.M ? a.wscale[i + e] : 0.f;
-      bias[e] = EPI == kOutDense && a.bias && i + e < a.M ? a.bias[i + e] : 0.f;
-    }
-    const uint32_t sums = smem_u32(ring) + (uint32_t)r * 4u;
-    const int left = min(per, a.rows - t0);
-    for (int c = (rank * kFinishWarps + wid - kFinishWarp0) * kUnit; c < left;
-         c += S * kFinishWarps * kUnit) {
-      int4 v[kUnit], lo[kUnit];
-#pragma unroll
-      for (int e = 0; e < kUnit; ++e) v[e] = lo[e] = make_int4(0, 0, 0, 0);
-#pragma unroll
-      for (int s0 = 0; s0 < kMaxSplit; s0 += 4) {
-        // (every load of four peers on its way before the first is used)
-        int4 pv[4][kUnit], pl[4][kUnit];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          if (s0 + s >= S) continue;
-          const uint32_t from = in_peer(sums, s0 + s) + (uint32_t)c * 512u;
-#pragma unroll
-          for (int e = 0; e < kUnit; ++e) {
-            pv[s][e] = peer_load(from + e * 512);
-            if (P == 2) pl[s][e] = peer_load(from + (per + e) * 512);
-          }
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          if (s0 + s >= S) continue;
-#pragma unroll
-          for (int e = 0; e < kUnit; ++e) {
-            add4(v[e], pv[s][e]);
-            if (P == 2) add4(lo[e], pl[s][e]);
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < kUnit; ++e)
-        if (c + e < left) finish_rows<EPI>(a, v[e], lo[e], ws, bias, i, t0 + c + e);
-    }
-  }
-  __syncwarp();
-  cluster_sync();  // (a CTA's sums stay until every peer has read them)
+  cluster_wait();  // (no CTA leaves while another may still add to its sums)
   if (wid == 2) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tcols)
@@ -354,12 +369,12 @@ int launch(const GemmArgs& a, const SplitPlan& p, bool after_rows, cudaStream_t 
               : byte_map(&wmap, a.w, a.K, a.M, a.ldw, 0, 0, kKStep, kHalfRows)))
     return EXTERND_ERR_CUDA;
   const int stage_bytes = kOperand + NT * kKStep + (CODES ? kCodeBytes : 0);
-  const int stages = std::min(kMaxStages, (kSplitSmemMax - 1024) / stage_bytes);
+  const int sums = (p.per + p.S - 1) / p.S * P * 512;
+  const int stages = std::min(kMaxStages, (kSplitSmemMax - 1024 - sums) / stage_bytes);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.MT * p.S), (unsigned)p.TT);
   cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes =
-      std::max(stages * stage_bytes + 1024, kSplitSmemMin);
+  cfg.dynamicSmemBytes = std::max(stages * stage_bytes + sums + 1024, kSplitSmemMin);
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -409,7 +424,7 @@ int resident_clusters(int dev, int S) {
 }  // namespace
 
 // The largest split whose clusters the device holds at once; false where there
-// is none.
+// is none, or none of two or more with a tile that is not narrow.
 bool split_plan(const GemmArgs& a, Epilogue epi, int dev, SplitPlan* p) {
   const int P = epi == kOutFactors ? 2 : 1;
   const int most = 256 / P, unit = 16 / P;
@@ -428,10 +443,9 @@ bool split_plan(const GemmArgs& a, Epilogue epi, int dev, SplitPlan* p) {
       least = steps;
     }
   }
-  // in units of 10 ns: a step of a narrow tile; the sums of S > 1 CTAs cross the
-  // cluster at some 10 bytes a cycle and CTA
-  p->cost = 600 + least * (16 + p->per * P / 16) + p->per * P * 3;
-  return p->S > 0;
+  // in units of 10 ns: a step of a narrow tile, and the sums that cross the cluster
+  p->cost = 400 + least * (16 + p->per * P / 16) + p->per * P * 2;
+  return p->S > 1 || (p->S == 1 && p->per * P <= 64);
 }
 
 int split_gemm(const GemmArgs& a, const SplitPlan& p, Epilogue epi, bool after_rows,
