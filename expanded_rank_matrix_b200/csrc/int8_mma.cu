@@ -111,39 +111,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
   fence_after();
   const uint32_t tmem = tmem_base;
   pdl_trigger();
-  pdl_wait();
 
   if (wid == 0) {
     if (elect_one()) {  // ---- TMA producer ----
       const uint32_t tx = 2u * (uint32_t)((CODES ? 0 : kOperand) + half * kKStep);
-      int i = 0;
-      for (int tile = pair; tile < tiles; tile += npairs) {
-        const int mt = tile % MT, tt = tile / MT;
-        const int wrow = mt * 256 + rank * kHalfRows;
-        const int trow = EPI == kOutFactors ? tt * per : tt * per + rank * half;
-        const int plane = EPI == kOutFactors ? rank : 0;
-        bool ok = true;
-        for (int k = 0; k < ksteps; ++k, ++i) {
+      auto weights = [&](int s, int k, int wrow) {
+        const uint32_t dst = smem_u32(ring + s * kStageBytes), bar = smem_u32(&bars.full[s]);
+        if (rank == 0) bar_expect(bar, tx);
+        if (CODES) {
+          const uint32_t cbar = smem_u32(&bars.codes[s]);
+          bar_expect(cbar, kCodeBytes);
+          tma_2d_own(dst + 2 * kOperand, &wmap, k * kCodeRow, wrow, cbar);
+        } else {
+          tma_2d(dst, &wmap, k * kKStep, wrow, in_leader(bar));
+        }
+      };
+      auto tokens = [&](int s, int k, int tt) {
+        tma_3d(smem_u32(ring + s * kStageBytes) + kOperand, &xmap, k * kKStep,
+               EPI == kOutFactors ? tt * per : tt * per + rank * half,
+               EPI == kOutFactors ? rank : 0, in_leader(smem_u32(&bars.full[s])));
+      };
+      // the first weights do not depend on the kernel in front
+      const int ahead = pair < tiles ? min(kStages, ksteps) : 0;
+      const int wrow0 = (pair % MT) * 256 + rank * kHalfRows;
+      for (int k = 0; k < ahead; ++k) weights(k, k, wrow0);
+      pdl_wait();
+      for (int k = 0; k < ahead; ++k) tokens(k, k, pair / MT);
+      int i = ahead;
+      bool ok = true;
+      for (int tile = pair; tile < tiles && ok; tile += npairs) {
+        const int wrow = (tile % MT) * 256 + rank * kHalfRows, tt = tile / MT;
+        for (int k = tile == pair ? ahead : 0; k < ksteps; ++k, ++i) {
           const int s = i % kStages;
           if (i >= kStages &&
               !bar_wait(smem_u32(&bars.empty[s]), ((i / kStages) + 1) & 1, ab, a.budget)) {
             ok = false;
             break;
           }
-          const uint32_t bar = smem_u32(&bars.full[s]);
-          const uint32_t dst = smem_u32(ring + s * kStageBytes);
-          if (rank == 0) bar_expect(bar, tx);
-          const uint32_t lbar = in_leader(bar);
-          if (CODES) {
-            const uint32_t cbar = smem_u32(&bars.codes[s]);
-            bar_expect(cbar, kCodeBytes);
-            tma_2d_own(dst + 2 * kOperand, &wmap, k * kCodeRow, wrow, cbar);
-          } else {
-            tma_2d(dst, &wmap, k * kKStep, wrow, lbar);
-          }
-          tma_3d(dst + kOperand, &xmap, k * kKStep, trow, plane, lbar);
+          weights(s, k, wrow);
+          tokens(s, k, tt);
         }
-        if (!ok) break;
       }
     }
   } else if (wid == 1) {
@@ -195,6 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     // ---- epilogue: warp w reads lanes 32 (w % 4) .., one half of the columns ----
     const int quad = wid & 3, ch = (wid - kEpiWarp0) >> 2;
     const int et = tid - kEpiWarp0 * 32;
+    pdl_wait();
     int seg = 0;
     for (int tile = pair; tile < tiles; tile += npairs, ++seg) {
       const int q = seg & 1;
@@ -318,10 +326,13 @@ int launch(const GemmArgs& a, bool after_rows, cudaStream_t st) {
 
 }  // namespace
 
-// Estimated time in units of 10 ns.
+// Estimated time in units of 10 ns, fitted over the shapes of split_plan's
+// (2560 x 2560: 7.0 us at 16 tokens, 7.5 at 256, 10.0 at 1000; 2560 x 9728: 16.2,
+// 18.7, 22.1).  The split kernel is taken where its estimate is below this.
 long long mma_cost(const GemmArgs& a, Epilogue epi, int nsm) {
   const PairPlan p = pair_plan(a, epi, nsm);
-  return 500 + p.rounds * ((a.K + kKStep - 1) / kKStep) * (16 + p.NT / 20);
+  const int step = epi == kOutDense ? 13 + p.NT * 6 / 100 : 19 + p.NT * 4 / 100;
+  return 430 + p.rounds * ((a.K + kKStep - 1) / kKStep) * step;
 }
 
 int mma_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st) {

@@ -443,8 +443,12 @@ bool split_plan(const GemmArgs& a, Epilogue epi, int dev, SplitPlan* p) {
       least = steps;
     }
   }
-  // in units of 10 ns: a step of a narrow tile, and the sums that cross the cluster
-  p->cost = 400 + least * (16 + p->per * P / 16) + p->per * P * 2;
+  // Units of 10 ns, fitted over 8 .. 1000 tokens of eight shapes (2560 x 2560: 4.8
+  // us at 16 tokens, 8.7 at 128, 12.3 at 256; 2560 x 9728: 7.4, 11.2, 15.9): a
+  // step, which the copies into the SM bound (codes: their unpacking), and the
+  // sums that cross the cluster.
+  const int NT = p->per * P;
+  p->cost = 320 + least * ((epi == kOutDense ? 26 : 30) + NT / 20) + (p->S > 1 ? NT * 31 / 10 : 0);
   return p->S > 1 || (p->S == 1 && p->per * P <= 64);
 }
 
