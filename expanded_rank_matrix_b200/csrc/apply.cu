@@ -280,12 +280,18 @@ cudaMemPool_t apply_pool(int dev) {
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
     cudaMemPool_t p = nullptr;
-    if (cudaMemPoolCreate(&p, &props) != cudaSuccess) {
+    // (the first call may come while a stream is being captured; creating a
+    // pool touches no stream, but only a relaxed thread may do it then)
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    cudaError_t made = cudaMemPoolCreate(&p, &props);
+    unsigned long long keep = ~0ull;
+    if (made == cudaSuccess) made = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (made != cudaSuccess) {
       cudaGetLastError();
       return nullptr;
     }
-    unsigned long long keep = ~0ull;
-    cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
     pools[dev] = p;
   }
   return pools[dev];

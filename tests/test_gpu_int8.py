@@ -1,5 +1,10 @@
 """The 8-bit inference operators (quantize_rows, matmul_i8, pack_codes,
 apply_i8) against plain 64-bit forms of their formulas.  Needs a B200."""
+import os
+import subprocess
+import sys
+import threading
+
 import pytest
 import torch
 
@@ -9,6 +14,7 @@ from tests import int8_ref as R
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FLOATS = [torch.float32, torch.float16, torch.bfloat16]
 
 
@@ -323,6 +329,44 @@ def test_apply_extreme_factors(t):
     assert X.sync_status() == X.OK
 
 
+@pytest.mark.parametrize("t", [1, 3, 20, 300, 6000])
+def test_apply_component_ties(t):
+    """Component sums that lie exactly between two steps of their scale: a
+    component of 65536 ones and tokens of norm 254 make z = 2, so the odd sums
+    are ties, which go to the even neighbour."""
+    n, k, m = 65536, 200, 70
+    C = _ternary(k, n, 1)
+    C[0] = 1
+    B = _ternary(k, m, 2)
+    D = torch.ones(k, device="cuda")
+    q = torch.zeros(t, n, dtype=torch.int8, device="cuda")
+    at = torch.randint(0, n, (t, 4), generator=_gen(3), device="cuda")
+    at = at // 4 * 4 + torch.arange(4, device="cuda")  # four places, never the same
+    sign = torch.randint(0, 2, (t, 4), generator=_gen(4), device="cuda") * 2 - 1
+    q.scatter_(1, at, (127 * sign).to(torch.int8))
+    s = torch.rand(t, generator=_gen(5), device="cuda")
+    f = X.Factors(R.planes(B), R.planes(C), D, None, m, n)
+    h, z = R.components(q[:50].double(), C.double(), D)
+    assert (z == 2).all() and bool((h % 1 == 0).all())
+    y = X.apply_i8(X.pack_codes(f), X.Quantized(q, s))
+    for i in range(0, t, 1000):
+        R.check(y[i:i + 1000], *R.factors(q[i:i + 1000], s[i:i + 1000], B.double(), C.double(), D))
+
+
+@pytest.mark.parametrize("t", [1, 4, 40, 3000])
+def test_apply_largest_ranks(t):
+    """The longest inner dimensions with every sum at its largest."""
+    n, k, m = 40, X.I8_MAX_INNER, 9
+    B, C = torch.ones(k, m, device="cuda"), torch.ones(k, n, device="cuda")
+    D = torch.ones(k, device="cuda")
+    q = torch.full((t, 48), 127, dtype=torch.int8, device="cuda")[:, :n]
+    s = torch.ones(t, device="cuda")
+    f = X.Factors(R.planes(B), R.planes(C), D, None, m, n)
+    y = X.apply_i8(X.pack_codes(f), X.Quantized(q, s))
+    ref, bound = R.factors(q[:1], s[:1], B.double(), C.double(), D)
+    R.check(y, ref.expand(t, m), bound.expand(t, m))
+
+
 @pytest.mark.parametrize("t", [1, 12, 100, 520])
 def test_apply_exact_in_batches(t):
     f, *_ = _factors(300, 200, 500, 1)
@@ -350,6 +394,19 @@ def test_many_rows_of_a_narrow_product():
     t, n, m = 70001, 16, 8
     x, w = _x(t, n, torch.float16, 1), _held(m, n, 2)
     R.check(X.matmul_i8(x, w), *R.dense(*R.rows(x), w.q, w.scale))
+
+
+def test_offsets_past_32_bits():
+    """Outputs and inputs of more than 2^31 elements."""
+    t, m, n = 65000, 40000, 32
+    x, w = _held(t, n, 1), _held(m, n, 2)
+    y = X.matmul_i8(x, w, out_dtype=torch.bfloat16)
+    for i in (0, 1, 33000, 53690, 53688, t - 1):  # 53687 m is just below 2^31
+        R.check(y[i:i + 1], *R.dense(x.q[i:i + 1], x.scale[i:i + 1], w.q, w.scale))
+    r = X.quantize_rows(y)
+    for i in (0, 53688, t - 1):
+        q, s = R.rows(y[i:i + 1])
+        assert torch.equal(r.q[i:i + 1].double(), q) and torch.equal(r.scale[i:i + 1].double(), s)
 
 
 # --- together, streams, graphs -----------------------------------------------
@@ -457,6 +514,62 @@ def test_captured_and_replayed(t):
             R.check(outs[i][0], *R.dense(q, s, w.q, w.scale))
             R.check(outs[i][1], *R.factors(q, s, B, C, D))
     del graphs
+
+
+def test_first_call_captured(tmp_path):
+    """A graph may hold the first calls that a process makes."""
+    code = """
+import torch
+from expanded_rank_matrix_b200 import externd as X
+from tests import int8_ref as R
+x = torch.randn(%d, 256, device='cuda')
+wq = torch.randint(-127, 128, (64, 256), device='cuda', dtype=torch.int8)
+w = X.Quantized(wq, torch.rand(64, device='cuda'))
+q, s = R.rows(x)
+torch.cuda.synchronize()
+f = X.Factors(torch.full((96, 2, 2), 5, dtype=torch.int32, device='cuda'),
+              torch.full((96, 2, 8), 3, dtype=torch.int32, device='cuda'),
+              torch.rand(96, device='cuda'), None, 64, 256)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    c = X.pack_codes(f)
+    y = X.matmul_i8(x, w)
+    z = X.apply_i8(c, x)
+g.replay()
+torch.cuda.synchronize()
+R.check(y, *R.dense(q, s, w.q, w.scale))
+R.check(z, *R.factors(q, s, R.codes(f.packed_B, 64), R.codes(f.packed_C, 256), f.D))
+print('captured')
+"""
+    for t in (1, 60, 3000):
+        r = subprocess.run([sys.executable, "-c", code % t], cwd=ROOT, capture_output=True, text=True,
+                           timeout=120)
+        assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_threads_at_once():
+    """Calls from two host threads, each on its own stream."""
+    f, *_ = _factors(300, 200, 500, 1)
+    c = X.pack_codes(f)
+    xs = [_x(t, 200, torch.float32, t) for t in (1, 90)]
+    want = [X.apply_i8(c, x) for x in xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(x, y):
+        st = torch.cuda.Stream()
+        for _ in range(50):
+            got = X.apply_i8(c, x, stream=st)
+            st.synchronize()
+            if not torch.equal(got, y):
+                bad.append(1)
+    threads = [threading.Thread(target=work, args=a) for a in zip(xs, want)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not bad
 
 
 def test_binding_refusals():
