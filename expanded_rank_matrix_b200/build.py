@@ -1,14 +1,17 @@
-"""Builds libexternd.so (sm_100a) in-tree from csrc/*.cu with nvcc."""
+"""Builds libexternd.so (sm_100a) in-tree from csrc/*.cu with nvcc, and the
+native part of the Python binding (_calls.so) from csrc/calls.cpp."""
 from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libexternd.so")
+CALLS = os.path.join(HERE, "_calls.so")  # the native part of the Python binding
 # (-static-global-template-stub=false: the sequential kernel template is
 # instantiated in its own units and launched from seq_als.cu)
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
@@ -17,6 +20,34 @@ NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", 
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+
+
+def _stale_calls() -> bool:
+    deps = (os.path.join(CSRC, "calls.cpp"), os.path.join(HERE, "..", "include", "externd.h"))
+    return not os.path.exists(CALLS) or any(os.path.getmtime(d) > os.path.getmtime(CALLS)
+                                            for d in deps)
+
+
+def build_calls() -> str:
+    """Builds the module that marshals the 8-bit calls between torch and the C
+    ABI (it is given the library's entry points when that is loaded)."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    nvcc = os.environ.get("NVCC") or shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    inc = [os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = CALLS + ".tmp"
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    os.path.join(CSRC, "calls.cpp"), "-o", tmp, *(f"-I{i}" for i in inc),
+                    "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+                    "-ltorch_cuda", "-ltorch", "-ltorch_python"], check=True)
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 def _stale() -> bool:
@@ -29,6 +60,8 @@ def _stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    if force or _stale_calls():
+        build_calls()
     if not force and not _stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")

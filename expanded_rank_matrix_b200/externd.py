@@ -40,6 +40,7 @@ EXPORTS = ("externd_rank", "externd_decompose", "externd_decompose_ex", "externd
            "externd_pack_codes", "externd_ternary_apply_i8")
 
 _lib = None
+_calls = None  # the 8-bit calls' marshalling, bound to the library
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 
@@ -52,7 +53,7 @@ class ExterndError(RuntimeError):
 
 def load(path: str = LIB_PATH):
     """Loads the library (no GPU needed) and declares the signatures."""
-    global _lib
+    global _lib, _calls
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -104,6 +105,13 @@ def load(path: str = LIB_PATH):
     L.externd_sync_status.restype = ctypes.c_int
     L.externd_release_cache.argtypes = []
     L.externd_release_cache.restype = ctypes.c_int
+    try:
+        from . import _calls as native
+    except ImportError as e:
+        raise RuntimeError("_calls.so is not built; run __graft_entry__.build()") from e
+    native.bind(*(ctypes.cast(f, _vp).value for f in (
+        L.externd_quantize_rows, L.externd_matmul_i8, L.externd_ternary_apply_i8)))
+    _calls = native
     _lib = L
     return L
 
@@ -319,7 +327,6 @@ I8_MAX_INNER = 131071
 I8_MAX_OUT = 1 << 24
 
 F32, F16, BF16, I8 = 0, 1, 2, 3
-_TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
 
 def _device_of(t: torch.Tensor, *others) -> int:
@@ -333,34 +340,12 @@ def _device_of(t: torch.Tensor, *others) -> int:
     return index
 
 
-def _on(index: int, stream: Optional[torch.cuda.Stream]):
-    """Context in which the tensors' device, and a given stream, are current:
-    what is allocated or copied inside belongs to the stream of the launch."""
-    if stream is None:
-        return torch.cuda.device(index)
+def _elsewhere(index: int, stream: torch.cuda.Stream):
+    """Context in which a given stream is current: what a call allocates or
+    copies inside belongs to the stream of its launches."""
     if stream.device_index != index:
         raise ValueError("the stream belongs to another device than the tensors")
     return torch.cuda.stream(stream)
-
-
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-
-
-def _matrix(X: torch.Tensor):
-    """(matrix of X's rows, distance between rows): X [..., n] itself where its
-    rows lie at one distance and their elements side by side, else a copy."""
-    n = X.shape[-1]
-    if n == 0:
-        raise ValueError("expected at least one column")
-    if X.is_contiguous():
-        return X if X.dim() == 2 else X.view(-1, n), n
-    M = X if X.dim() == 2 else X.reshape(-1, n)
-    rows = M.shape[0]
-    if (n > 1 and M.stride(1) != 1) or (rows > 1 and M.stride(0) < n):
-        M = M.contiguous()
-    # (the stride of a single row means nothing)
-    return M, M.stride(0) if rows > 1 else n
 
 
 def _vector(v: torch.Tensor, length: int, what: str) -> torch.Tensor:
@@ -392,64 +377,32 @@ class Quantized:
             out = torch.empty((rows, ld), dtype=torch.int8, device=q.device)[:, :n]
             out.copy_(q)
             q = out
-        self._set(q, _vector(self.scale, rows, "scale"), ld, _device_of(q, self.scale))
+        self._set(q, _vector(self.scale, rows, "scale"))
+        _device_of(q, self.scale)
 
-    def _set(self, q, scale, ld, device):
+    def _set(self, q, scale):
         d = self.__dict__
-        d["q"], d["scale"], d["_device"] = q, scale, device
-        # what every call passes on: address, row distance, the scales' address
-        d["_raw"] = q.data_ptr(), ld, scale.data_ptr()
+        d["q"], d["scale"] = q, scale
 
 
 def quantize_rows(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> Quantized:
     """Symmetric 8-bit quantisation of the rows of X [..., n] (fp32, fp16 or
     bf16) with one scale a row (externd_quantize_rows): tokens of activations,
     output channels of a weight matrix."""
-    kind = _TYPES.get(X.dtype)
-    if kind is None or X.dim() == 0:
-        raise ValueError("X must be an fp32, fp16 or bf16 tensor of at least one dimension")
-    device = _device_of(X)
-    if stream is not None or device != _current_device():
-        with _on(device, stream):
+    if stream is not None:
+        with _elsewhere(X.get_device(), stream):
             return quantize_rows(X)
-    M, ldx = _matrix(X)
-    rows, n = M.shape
-    ldq = (n + 15) // 16 * 16
-    q = M.new_empty(rows, ldq, dtype=torch.int8)
-    scale = M.new_empty(rows, dtype=torch.float32)
-    rc = load().externd_quantize_rows(M.data_ptr(), kind, ldx, rows, n, q.data_ptr(), ldq,
-                                      scale.data_ptr(), _raw_stream(device))
-    if rc != OK:
-        raise ExterndError(rc, "externd_quantize_rows")
+    r = (_calls or _loaded()).quantize_rows(X)
+    if r.__class__ is int:
+        raise ExterndError(r, "externd_quantize_rows")
     out = Quantized.__new__(Quantized)
-    out._set(q if ldq == n else q[:, :n], scale, ldq, device)
+    out._set(*r)
     return out
 
 
-def _activations(X, n: int, device: int, out_dtype):
-    """(the activations' address, type, row distance, scales' address, rows, the
-    output's number of type, and the output's leading sizes and a tensor to
-    allocate it from, and its type) for an 8-bit product."""
-    if X.__class__ is Quantized:
-        M, kind, where, dt = X.q, I8, X._device, out_dtype or torch.float32
-        lead = (M.shape[0],)
-        at, ldx, s = X._raw
-    else:
-        kind = _TYPES.get(X.dtype)
-        if kind is None or X.dim() == 0:
-            raise ValueError("X must be Quantized, or an fp32, fp16 or bf16 tensor of at least "
-                             "one dimension")
-        (M, ldx), s, lead = _matrix(X), None, X.shape[:-1]
-        at, where, dt = M.data_ptr(), X.get_device(), out_dtype or X.dtype
-    rows, cols = M.shape
-    if where != device:
-        raise ValueError("expected tensors on one CUDA device")
-    if cols != n:
-        raise ValueError(f"X must have {n} columns")
-    out = _TYPES.get(dt)
-    if out is None:
-        raise ValueError("out_dtype must be fp32, fp16 or bf16")
-    return at, kind, ldx, s, rows, out, lead, M, dt
+def _loaded():
+    load()
+    return _calls
 
 
 def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=None,
@@ -459,25 +412,14 @@ def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=No
     fp16 or bf16, quantised within the call, or Quantized rows (shared by
     several products).  The output is [..., m] of out_dtype (default: X's
     type; fp32 for Quantized)."""
-    device = W._device
-    if stream is not None or device != _current_device():
-        with _on(device, stream):
+    if stream is not None:
+        with _elsewhere(W.q.get_device(), stream):
             return matmul_i8(X, W, bias, out_dtype)
-    m, n = W.q.shape
-    at, kind, ldx, s, rows, out, lead, M, dt = _activations(X, n, device, out_dtype)
-    b = None
-    if bias is not None:
-        bias = _vector(bias, m, "bias")
-        if bias.get_device() != device:
-            raise ValueError("expected tensors on one CUDA device")
-        b = bias.data_ptr()
-    Y = M.new_empty(*lead, m, dtype=dt)
-    w, ldw, ws = W._raw
-    rc = load().externd_matmul_i8(at, kind, ldx, s, w, ldw, ws, b, rows, n, m, Y.data_ptr(), out, m,
-                                  _raw_stream(device))
-    if rc != OK:
-        raise ExterndError(rc, "externd_matmul_i8")
-    return Y
+    x, s = (X.q, X.scale) if X.__class__ is Quantized else (X, None)
+    r = (_calls or _loaded()).matmul_i8(x, s, W.q, W.scale, bias, out_dtype)
+    if r.__class__ is int:
+        raise ExterndError(r, "externd_matmul_i8")
+    return r
 
 
 def code_words(length: int) -> int:
@@ -508,18 +450,18 @@ class FactorCodes:
                                (self.D, (k,), torch.float32), (self.bound, (1,), torch.float32)):
             if t.dtype != kind or t.shape != shape or not t.is_contiguous():
                 raise ValueError("codes, D and bound must be as pack_codes returns them")
-        tensors = self.codes_B, self.codes_C, self.D, self.bound
-        self.__dict__["_device"] = _device_of(*tensors)
-        # what every call passes on
-        self.__dict__["_raw"] = (*(t.data_ptr() for t in tensors), self.m, self.n, k)
+        _device_of(self.D, self.codes_B, self.codes_C, self.bound)
 
 
 def pack_codes(f: Factors, stream: Optional[torch.cuda.Stream] = None) -> FactorCodes:
     """Lays factors out once for apply_i8 (externd_pack_codes): those of a
     decomposition, or its first components (truncate)."""
     device = _device_of(f.D, f.packed_B, f.packed_C)
-    if stream is not None or device != _current_device():
-        with _on(device, stream):
+    if stream is not None:
+        with _elsewhere(device, stream):
+            return pack_codes(f)
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
             return pack_codes(f)
     k = f.k
     D, pB, pC = f.D.contiguous(), f.packed_B.contiguous(), f.packed_C.contiguous()
@@ -532,7 +474,7 @@ def pack_codes(f: Factors, stream: Optional[torch.cuda.Stream] = None) -> Factor
     bound = D.new_empty(1)
     rc = load().externd_pack_codes(pB.data_ptr(), pC.data_ptr(), D.data_ptr(), f.m, f.n, k,
                                    cB.data_ptr(), cC.data_ptr(), bound.data_ptr(),
-                                   _raw_stream(device))
+                                   _stream(None))
     if rc != OK:
         raise ExterndError(rc, "externd_pack_codes")
     return FactorCodes(cB, cC, D, bound, f.m, f.n)
@@ -542,17 +484,14 @@ def apply_i8(c: FactorCodes, X, out_dtype=None,
              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """X (B diag(D) C)^T on 8-bit activations, from the packed codes
     (externd_ternary_apply_i8).  X and out_dtype as for matmul_i8."""
-    device = c._device
-    if stream is not None or device != _current_device():
-        with _on(device, stream):
+    if stream is not None:
+        with _elsewhere(c.D.get_device(), stream):
             return apply_i8(c, X, out_dtype)
-    at, kind, ldx, s, rows, out, lead, M, dt = _activations(X, c.n, device, out_dtype)
-    Y = M.new_empty(*lead, c.m, dtype=dt)
-    rc = load().externd_ternary_apply_i8(*c._raw, at, kind, ldx, s, rows, Y.data_ptr(), out, c.m,
-                                         _raw_stream(device))
-    if rc != OK:
-        raise ExterndError(rc, "externd_ternary_apply_i8")
-    return Y
+    x, s = (X.q, X.scale) if X.__class__ is Quantized else (X, None)
+    r = (_calls or _loaded()).apply_i8(c.codes_B, c.codes_C, c.D, c.bound, c.n, x, s, out_dtype)
+    if r.__class__ is int:
+        raise ExterndError(r, "externd_ternary_apply_i8")
+    return r
 
 
 PROBE_SMEM = 0
