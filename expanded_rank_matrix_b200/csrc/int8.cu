@@ -26,15 +26,15 @@ constexpr int64_t kPassRows = 4096;
 
 int64_t type_size(int type) { return type == EXTERND_F32 ? 4 : type == EXTERND_I8 ? 1 : 2; }
 
-int gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st) {
-  if (a.rows <= kTokens) return token_gemm(a, epi, after_rows, st);
+int gemm(const GemmArgs& a, Epilogue epi, cudaStream_t st) {
+  if (a.rows <= kTokens) return token_gemm(a, epi, st);
   int dev = 0, nsm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EXTERND_ERR_CUDA;
   cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
   SplitPlan p;
   if (split_plan(a, epi, dev, &p) && p.cost < mma_cost(a, epi, nsm))
-    return split_gemm(a, p, epi, after_rows, st);
-  return mma_gemm(a, epi, after_rows, st);
+    return split_gemm(a, p, epi, st);
+  return mma_gemm(a, epi, st);
 }
 
 // The device's status word (its address does not change; looking it up costs
@@ -124,7 +124,8 @@ int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int
       a.ldx = ldq;
       a.xscale = s;
     }
-    if (rc == EXTERND_OK) rc = gemm(a, kOutDense, xtype != EXTERND_I8, st);
+    a.early = xtype != EXTERND_I8;
+    if (rc == EXTERND_OK) rc = gemm(a, kOutDense, st);
   }
   return ws.release(rc);
 }
@@ -176,14 +177,16 @@ int factors(const uint32_t* codes_B, const uint32_t* codes_C, const float* D, co
     a.w = codes_C; a.ldw = code_words(n); a.wscale = D;
     a.M = (int)k; a.K = (int)n;
     a.y = h; a.ldy = ldh; a.plane = plane;
-    rc = token ? token_raw(a, kOutPlanes, st) : gemm(a, kOutPlanes, true, st);
+    a.early = !token;
+    rc = token ? token_raw(a, kOutPlanes, st) : gemm(a, kOutPlanes, st);
     if (rc != EXTERND_OK) break;
     a.x = h; a.ldx = ldh;
     a.w = codes_B; a.ldw = code_words(k);
     a.M = (int)m; a.K = (int)k;
     a.y = (char*)Y + r0 * ldy * type_size(ytype);
     a.ytype = ytype; a.ldy = ldy;
-    rc = gemm(a, kOutFactors, true, st);
+    a.early = true;
+    rc = gemm(a, kOutFactors, st);
   }
   return ws.release(rc);
 }

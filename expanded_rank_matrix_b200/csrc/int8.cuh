@@ -58,6 +58,7 @@ struct GemmArgs {
   const float* rho;
   float* scale_out;
   float* z_out;
+  bool early;  // the kernel in front is of the same call: see pdl_wait
   int* status;
   long long budget;
 };
@@ -144,6 +145,14 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return r;
 }
 
+// Programmatic dependent launch.  Every kernel of these operators may start
+// while the one in front of it on the stream still runs, and waits (pdl_wait)
+// before it reads or writes anything that is not its own; so launches and
+// prologues pass behind the kernel in front.  A call's first kernel lets the
+// next one start (pdl_trigger) only after its own wait: when the call's later
+// kernels start, everything in front of the call has ended, so they may read
+// the call's weights, which none of its own kernels write, before their wait
+// (GemmArgs::early).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -16,22 +16,43 @@ int row_norms(const int8_t* Q, int64_t ldq, int64_t rows, int64_t n, const float
               cudaStream_t st);
 int pack_codes(const uint32_t* pB, const uint32_t* pC, const float* D, int64_t m, int64_t n,
                int64_t k, uint32_t* codes_B, uint32_t* codes_C, float* rho, cudaStream_t st);
-// The products.  after_rows: the launch follows one of this library's kernels
-// on the stream that lets it start early (it waits for that kernel's end
-// before it reads its results).
+// Launches a kernel that waits for the one in front by itself (pdl_wait).
+template <typename... P, typename... A>
+int launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
+                   cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return EXTERND_ERR_CUDA;
+  }
+  return EXTERND_OK;
+}
+
+// The products.
 constexpr int kTokens = 4;          // most rows of token_gemm
 constexpr int kTokenInner = 32768;  // longest token that token_raw quantises
 int token_raw(const GemmArgs& a, Epilogue epi, cudaStream_t st);
-int token_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
+int token_gemm(const GemmArgs& a, Epilogue epi, cudaStream_t st);
 struct SplitPlan {
   int MT, TT, per, S;  // tiles of 128 weight rows, of `per` tokens, CTAs that split K
   long long cost;      // estimated time, as mma_cost
 };
 bool split_plan(const GemmArgs& a, Epilogue epi, int dev, SplitPlan* p);
-int split_gemm(const GemmArgs& a, const SplitPlan& p, Epilogue epi, bool after_rows,
-               cudaStream_t st);
+int split_gemm(const GemmArgs& a, const SplitPlan& p, Epilogue epi, cudaStream_t st);
 long long mma_cost(const GemmArgs& a, Epilogue epi, int nsm);
-int mma_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st);
+int mma_gemm(const GemmArgs& a, Epilogue epi, cudaStream_t st);
 int quantize(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8_t* Q, int64_t ldq,
              float* scale, cudaStream_t st);
 int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W, int64_t ldw,

@@ -110,7 +110,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
   cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_base;
-  pdl_trigger();
+  if (a.early) pdl_trigger();
 
   if (wid == 0) {
     if (elect_one()) {  // ---- TMA producer ----
@@ -131,7 +131,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
                EPI == kOutFactors ? tt * per : tt * per + rank * half,
                EPI == kOutFactors ? rank : 0, in_leader(smem_u32(&bars.full[s])));
       };
-      // the first weights do not depend on the kernel in front
+      if (!a.early) {
+        pdl_wait();
+        pdl_trigger();
+      }
       const int ahead = pair < tiles ? min(kStages, ksteps) : 0;
       const int wrow0 = (pair % MT) * 256 + rank * kHalfRows;
       for (int k = 0; k < ahead; ++k) weights(k, k, wrow0);
@@ -284,7 +287,7 @@ PairPlan pair_plan(const GemmArgs& a, Epilogue epi, int nsm) {
 }
 
 template <bool CODES, Epilogue EPI>
-int launch(const GemmArgs& a, bool after_rows, cudaStream_t st) {
+int launch(const GemmArgs& a, cudaStream_t st) {
   int dev = 0, nsm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return EXTERND_ERR_CUDA;
   cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
@@ -306,22 +309,9 @@ int launch(const GemmArgs& a, bool after_rows, cudaStream_t st) {
       !(CODES ? byte_map(&wmap, a.w, 4 * a.ldw, a.M, 4 * a.ldw, 0, 0, kCodeRow, kHalfRows)
               : byte_map(&wmap, a.w, a.K, a.M, a.ldw, 0, 0, kKStep, kHalfRows)))
     return EXTERND_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2u * (unsigned)std::min<long long>(pairs, MT * TT));
-  cfg.blockDim = dim3(mma_threads(CODES));
-  cfg.dynamicSmemBytes = kMmaSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = after_rows ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, mma_kernel<CODES, EPI>, xmap, wmap, a, NT, MT, (int)TT) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return EXTERND_ERR_CUDA;
-  }
-  return EXTERND_OK;
+  return launch_chained(mma_kernel<CODES, EPI>,
+                        dim3(2u * (unsigned)std::min<long long>(pairs, MT * TT)), mma_threads(CODES),
+                        kMmaSmem, 0, st, xmap, wmap, a, NT, MT, (int)TT);
 }
 
 }  // namespace
@@ -335,10 +325,10 @@ long long mma_cost(const GemmArgs& a, Epilogue epi, int nsm) {
   return 430 + p.rounds * ((a.K + kKStep - 1) / kKStep) * step;
 }
 
-int mma_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st) {
-  if (epi == kOutDense) return launch<false, kOutDense>(a, after_rows, st);
-  if (epi == kOutPlanes) return launch<true, kOutPlanes>(a, after_rows, st);
-  return launch<true, kOutFactors>(a, after_rows, st);
+int mma_gemm(const GemmArgs& a, Epilogue epi, cudaStream_t st) {
+  if (epi == kOutDense) return launch<false, kOutDense>(a, st);
+  if (epi == kOutPlanes) return launch<true, kOutPlanes>(a, st);
+  return launch<true, kOutFactors>(a, st);
 }
 
 }  // namespace i8

@@ -42,6 +42,7 @@ template <typename T, int H, bool VEC, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rows_kernel(const RowArgs<T> a) {
   constexpr int E = 16 / sizeof(T);
   __shared__ uint32_t red[2][32];
+  pdl_wait();
   pdl_trigger();
   const int G = WARP ? 32 : (int)blockDim.x;
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(256) row_norm_kernel(const int8_t* __restrict_
                                                        const float* __restrict__ rho,
                                                        float* __restrict__ z) {
   __shared__ uint32_t red[32];
+  pdl_wait();
   pdl_trigger();
   const int64_t row = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
   if (row >= rows) return;
@@ -155,11 +157,8 @@ template <typename T, int H, bool WARP>
 int launch_rows_h(const RowArgs<T>& a, int threads, cudaStream_t st) {
   const bool vec = ((uintptr_t)a.x & 15) == 0 && (a.ldx * (int64_t)sizeof(T)) % 16 == 0;
   const int64_t grid = WARP ? (a.rows + kWarpRows - 1) / kWarpRows : a.rows;
-  if (vec)
-    rows_kernel<T, H, true, WARP><<<(unsigned)grid, threads, 0, st>>>(a);
-  else
-    rows_kernel<T, H, false, WARP><<<(unsigned)grid, threads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? EXTERND_OK : EXTERND_ERR_CUDA;
+  return launch_chained(vec ? rows_kernel<T, H, true, WARP> : rows_kernel<T, H, false, WARP>,
+                        dim3((unsigned)grid), threads, 0, 0, st, a);
 }
 
 // HBM stays busy through the bytes in flight on an SM and many small CTAs
@@ -259,12 +258,11 @@ int quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, int64_t n,
 int row_norms(const int8_t* Q, int64_t ldq, int64_t rows, int64_t n, const float* rho, float* z,
               cudaStream_t st) {
   if (n <= 2048)
-    row_norm_kernel<true><<<(unsigned)((rows + kWarpRows - 1) / kWarpRows), 32 * kWarpRows, 0, st>>>(
-        Q, ldq, rows, (int)n, rho, z);
-  else
-    row_norm_kernel<false><<<(unsigned)rows, std::min<int>((int)(n + 2047) / 2048 * 32, 256), 0, st>>>(
-        Q, ldq, rows, (int)n, rho, z);
-  return cudaGetLastError() == cudaSuccess ? EXTERND_OK : EXTERND_ERR_CUDA;
+    return launch_chained(row_norm_kernel<true>, dim3((unsigned)((rows + kWarpRows - 1) / kWarpRows)),
+                          32 * kWarpRows, 0, 0, st, Q, ldq, rows, (int)n, rho, z);
+  return launch_chained(row_norm_kernel<false>, dim3((unsigned)rows),
+                        std::min((int)(n + 2047) / 2048 * 32, 256), 0, 0, st, Q, ldq, rows, (int)n,
+                        rho, z);
 }
 
 int pack_codes(const uint32_t* pB, const uint32_t* pC, const float* D, int64_t m, int64_t n,

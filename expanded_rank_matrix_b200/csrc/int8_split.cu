@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     abort_flag = 0;
     // the weights of the first ring fill, before anything else
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&xmap) : "memory");
+    if (!a.early) pdl_wait();
     for (int i = 0; i < ahead; ++i) weights(i);
   }
   fence_before();
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   } else {
     cluster_arrive_relaxed();
   }
-  pdl_trigger();
+  if (a.early) pdl_trigger();
 
   if (wid == 0) {
     if (producer) {  // ---- TMA producer ----
@@ -226,7 +227,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         for (int p = 0; p < P; ++p)
           tma_3d_own(dst + p * per * kKStep, &xmap, (k0 + i) * kKStep, t0, p, bar);
       };
-      pdl_wait();
+      if (a.early)
+        pdl_wait();
+      else
+        pdl_trigger();
       for (int i = 0; i < ahead; ++i) tokens(i);
       for (int i = ahead; i < steps; ++i) {
         const int s = i % stages;
@@ -297,6 +301,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       }
     }
     // ---- the CTA's own tokens: a warp each, a lane four neighbouring rows ----
+    pdl_wait();
     const int r = 4 * lane, i = i0 + r;
     float ws[4], bias[4];
 #pragma unroll
@@ -304,7 +309,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       ws[e] = EPI != kOutFactors && i + e < a.M ? a.wscale[i + e] : 0.f;
       bias[e] = EPI == kOutDense && a.bias && i + e < a.M ? a.bias[i + e] : 0.f;
     }
-    pdl_wait();
     int j = wid - kFinishWarp0;
     float s = 0.f, z = 0.f;
     if (j < mine) {
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 }
 
 template <bool CODES, Epilogue EPI>
-int launch(const GemmArgs& a, const SplitPlan& p, bool after_rows, cudaStream_t st) {
+int launch(const GemmArgs& a, const SplitPlan& p, cudaStream_t st) {
   constexpr int P = EPI == kOutFactors ? 2 : 1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EXTERND_ERR_CUDA;
@@ -371,25 +375,9 @@ int launch(const GemmArgs& a, const SplitPlan& p, bool after_rows, cudaStream_t 
   const int stage_bytes = kOperand + NT * kKStep + (CODES ? kCodeBytes : 0);
   const int sums = (p.per + p.S - 1) / p.S * P * 512;
   const int stages = std::min(kMaxStages, (kSplitSmemMax - 1024 - sums) / stage_bytes);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.MT * p.S), (unsigned)p.TT);
-  cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = std::max(stages * stage_bytes + sums + 1024, kSplitSmemMin);
-  cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)p.S;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = after_rows ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, split_kernel<CODES, EPI>, xmap, wmap, a, NT, p.S, stages) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return EXTERND_ERR_CUDA;
-  }
-  return EXTERND_OK;
+  const int smem = std::max(stages * stage_bytes + sums + 1024, kSplitSmemMin);
+  return launch_chained(split_kernel<CODES, EPI>, dim3((unsigned)(p.MT * p.S), (unsigned)p.TT),
+                        kSplitThreads, smem, p.S, st, xmap, wmap, a, NT, p.S, stages);
 }
 
 // Clusters of S CTAs, one CTA per SM, that the device holds at once.
@@ -452,11 +440,11 @@ bool split_plan(const GemmArgs& a, Epilogue epi, int dev, SplitPlan* p) {
   return p->S > 1 || (p->S == 1 && p->per * P <= 64);
 }
 
-int split_gemm(const GemmArgs& a, const SplitPlan& p, Epilogue epi, bool after_rows,
+int split_gemm(const GemmArgs& a, const SplitPlan& p, Epilogue epi,
                cudaStream_t st) {
-  if (epi == kOutDense) return launch<false, kOutDense>(a, p, after_rows, st);
-  if (epi == kOutPlanes) return launch<true, kOutPlanes>(a, p, after_rows, st);
-  return launch<true, kOutFactors>(a, p, after_rows, st);
+  if (epi == kOutDense) return launch<false, kOutDense>(a, p, st);
+  if (epi == kOutPlanes) return launch<true, kOutPlanes>(a, p, st);
+  return launch<true, kOutFactors>(a, p, st);
 }
 
 }  // namespace i8

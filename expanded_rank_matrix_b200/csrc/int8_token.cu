@@ -133,9 +133,10 @@ __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
       }
     }
   };
-  fetch(0);
-  pdl_trigger();
+  if (a.early) fetch(0);
   pdl_wait();
+  pdl_trigger();
+  if (!a.early) fetch(0);
   float scale = 0.f, z = 0.f;
   if constexpr (FUSED) {
     uint32_t squares = 0u;
@@ -227,43 +228,31 @@ __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
 }
 
 template <bool CODES, Epilogue EPI, int R, int T, typename RAW, bool VEC>
-int launch_r(const GemmArgs& a, bool after_rows, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.M + R * kTkThreads / 32 - 1) / (R * kTkThreads / 32)));
-  cfg.blockDim = dim3(kTkThreads);
-  cfg.dynamicSmemBytes = sizeof(RAW) > 1 ? (a.K + 15) / 16 * 16 : 0;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = after_rows ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, token_kernel<CODES, EPI, R, T, RAW, VEC>, a) != cudaSuccess) {
-    cudaGetLastError();
-    return EXTERND_ERR_CUDA;
-  }
-  return EXTERND_OK;
+int launch_r(const GemmArgs& a, cudaStream_t st) {
+  constexpr int per = R * kTkThreads / 32;
+  return launch_chained(token_kernel<CODES, EPI, R, T, RAW, VEC>, dim3((unsigned)((a.M + per - 1) / per)),
+                        kTkThreads, sizeof(RAW) > 1 ? (a.K + 15) / 16 * 16 : 0, 0, st, a);
 }
 
 // More rows a warp reuse a lane's activations; fewer keep all SMs at work.
 template <bool CODES, Epilogue EPI, int T, typename RAW, bool VEC>
-int launch(const GemmArgs& a, bool after_rows, cudaStream_t st) {
-  if (a.M >= 8192) return launch_r<CODES, EPI, 4, T, RAW, VEC>(a, after_rows, st);
-  if (a.M >= 4096) return launch_r<CODES, EPI, 2, T, RAW, VEC>(a, after_rows, st);
-  return launch_r<CODES, EPI, 1, T, RAW, VEC>(a, after_rows, st);
+int launch(const GemmArgs& a, cudaStream_t st) {
+  if (a.M >= 8192) return launch_r<CODES, EPI, 4, T, RAW, VEC>(a, st);
+  if (a.M >= 4096) return launch_r<CODES, EPI, 2, T, RAW, VEC>(a, st);
+  return launch_r<CODES, EPI, 1, T, RAW, VEC>(a, st);
 }
 
 template <bool CODES, Epilogue EPI>
-int launch_i8(const GemmArgs& a, bool after_rows, cudaStream_t st) {
-  if (a.rows == 1) return launch<CODES, EPI, 1, int8_t, true>(a, after_rows, st);
-  if (a.rows == 2) return launch<CODES, EPI, 2, int8_t, true>(a, after_rows, st);
-  return launch<CODES, EPI, 4, int8_t, true>(a, after_rows, st);
+int launch_i8(const GemmArgs& a, cudaStream_t st) {
+  if (a.rows == 1) return launch<CODES, EPI, 1, int8_t, true>(a, st);
+  if (a.rows == 2) return launch<CODES, EPI, 2, int8_t, true>(a, st);
+  return launch<CODES, EPI, 4, int8_t, true>(a, st);
 }
 
 template <bool CODES, Epilogue EPI, typename RAW>
 int launch_raw(const GemmArgs& a, cudaStream_t st) {
-  return ((uintptr_t)a.raw & 15) == 0 ? launch<CODES, EPI, 1, RAW, true>(a, false, st)
-                                      : launch<CODES, EPI, 1, RAW, false>(a, false, st);
+  return ((uintptr_t)a.raw & 15) == 0 ? launch<CODES, EPI, 1, RAW, true>(a, st)
+                                      : launch<CODES, EPI, 1, RAW, false>(a, st);
 }
 
 template <bool CODES, Epilogue EPI>
@@ -280,10 +269,10 @@ int token_raw(const GemmArgs& a, Epilogue epi, cudaStream_t st) {
                           : launch_token<true, kOutPlanes>(a, st);
 }
 
-int token_gemm(const GemmArgs& a, Epilogue epi, bool after_rows, cudaStream_t st) {
-  if (epi == kOutDense) return launch_i8<false, kOutDense>(a, after_rows, st);
-  if (epi == kOutPlanes) return launch_i8<true, kOutPlanes>(a, after_rows, st);
-  return launch_i8<true, kOutFactors>(a, after_rows, st);
+int token_gemm(const GemmArgs& a, Epilogue epi, cudaStream_t st) {
+  if (epi == kOutDense) return launch_i8<false, kOutDense>(a, st);
+  if (epi == kOutPlanes) return launch_i8<true, kOutPlanes>(a, st);
+  return launch_i8<true, kOutFactors>(a, st);
 }
 
 }  // namespace i8

@@ -516,6 +516,74 @@ def test_captured_and_replayed(t):
     del graphs
 
 
+@pytest.mark.parametrize("t", [1, 3, 24, 200, 3000])
+def test_operands_written_just_before(t):
+    """Weights, scales and activations written by the kernels right in front of
+    a call, and results read right behind it, over and over: the kernels start
+    early and have to wait for what they read."""
+    m, n = 700, 1030
+    g = _gen(t)
+    src = [(torch.randint(-127, 128, (m, 1040), generator=g, device="cuda", dtype=torch.int8),
+            torch.rand(m, generator=g, device="cuda"), _x(t, n, torch.float32, 50 + i))
+           for i in range(3)]
+    fs = [_factors(300, n, 900, 60 + i) for i in range(3)]
+    packed = [X.pack_codes(f[0]) for f in fs]
+    want = [(X.matmul_i8(x, X.Quantized(w[:, :n], s)), X.apply_i8(c, x))
+            for (w, s, x), c in zip(src, packed)]
+    w, s, x = (v.clone() for v in src[0])
+    c = packed[0]
+    live = X.FactorCodes(c.codes_B.clone(), c.codes_C.clone(), c.D.clone(), c.bound.clone(), c.m, c.n)
+    torch.cuda.synchronize()
+    for r in range(30):
+        i = r % 3
+        for to, at in zip((w, s, x), src[i]):
+            to.copy_(at)
+        y = X.matmul_i8(x, X.Quantized(w[:, :n], s))
+        for name in ("codes_B", "codes_C", "D", "bound"):
+            getattr(live, name).copy_(getattr(packed[i], name))
+        z = X.apply_i8(live, x)
+        xq = X.quantize_rows(x)
+        y2, z2 = X.matmul_i8(xq, X.Quantized(w[:, :n], s)).clone(), X.apply_i8(live, xq).clone()
+        x.zero_()
+        w.zero_()
+        assert torch.equal(y, want[i][0]) and torch.equal(z, want[i][1])
+        assert torch.equal(y2, want[i][0]) and torch.equal(z2, want[i][1])
+
+
+@pytest.mark.parametrize("t", [1, 24, 3000])
+def test_captured_behind_a_join(t):
+    """Captured right behind a copy, a memset and two joined streams."""
+    w, x = _held(200, 100, 3), _x(t, 100, torch.float32, 1)
+    f, B, C, D = _factors(150, 100, 200, 1)
+    c = X.pack_codes(f)
+    src = x.clone()
+    X.matmul_i8(x, w)
+    X.apply_i8(c, x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        x.zero_()
+        with torch.cuda.stream(side):
+            y0 = X.matmul_i8(src, w)
+        main.wait_stream(side)
+        y1 = X.matmul_i8(x, w)
+        x.copy_(src)
+        y2 = X.matmul_i8(x, w)
+        z = X.apply_i8(c, x)
+    q, s = R.rows(src)
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        ref = R.dense(q, s, w.q, w.scale)
+        R.check(y0, *ref)
+        R.check(y2, *ref)
+        assert (y1 == 0).all()
+        R.check(z, *R.factors(q, s, B, C, D))
+
+
 def test_first_call_captured(tmp_path):
     """A graph may hold the first calls that a process makes."""
     code = """
