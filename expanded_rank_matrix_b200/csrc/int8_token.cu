@@ -40,16 +40,29 @@ __device__ __forceinline__ uint4 first_bytes(uint4 v, int left) {
   return v;
 }
 
-// The token's row quantised into shared memory (zeros up to a whole step),
-// its scale, and the sum of its squares; all threads of the CTA take part.
+// The token that a kernel quantises itself: the vectors of it that a thread
+// holds.  They are requested before any weights, behind which they would wait.
+constexpr int kTokenHeld = 2;
 template <typename T, bool VEC>
-__device__ __forceinline__ float quantize_token(const T* x, int n, int padded, unsigned char* xs,
-                                                uint32_t* red, uint32_t* squares, bool want) {
+__device__ __forceinline__ void load_token(const T* x, int n, T (&v)[kTokenHeld][16 / sizeof(T)]) {
+#pragma unroll
+  for (int h = 0; h < kTokenHeld; ++h)
+    load_vec<T, VEC>(x, first_of<T, VEC>(h, threadIdx.x, blockDim.x), n, blockDim.x, v[h]);
+}
+
+// Its row quantised into shared memory (zeros up to `padded`), its scale, and
+// the sum of its squares; all threads of the CTA take part.
+template <typename T, bool VEC>
+__device__ __forceinline__ float quantize_token(const T* x, const T (&v)[kTokenHeld][16 / sizeof(T)],
+                                                int n, int padded, unsigned char* xs, uint32_t* red,
+                                                uint32_t* squares, bool want) {
   constexpr int E = 16 / sizeof(T);
   const int G = blockDim.x, tid = threadIdx.x;
   uint32_t top = 0u;
+#pragma unroll
+  for (int h = 0; h < kTokenHeld; ++h) top = top_bits(top, v[h]);
 #pragma unroll 4
-  for (int h = 0; h * G * E < n; ++h) {
+  for (int h = kTokenHeld; h * G * E < n; ++h) {
     T u[E];
     load_vec<T, VEC>(x, first_of<T, VEC>(h, tid, G), n, G, u);
     top = top_bits(top, u);
@@ -59,12 +72,9 @@ __device__ __forceinline__ float quantize_token(const T* x, int n, int padded, u
   const bool safe = safe_scale(s);
   const float inv = safe ? __fdiv_rn(1.f, s) : 0.f;
   uint32_t sq = 0u, which = 0u;
-#pragma unroll 2
-  for (int h = 0; h * G * E < padded; ++h) {
+  auto emit = [&](int h, const T (&u)[E]) {
     const int j = first_of<T, VEC>(h, tid, G);
-    T u[E];
     uint32_t b[E];
-    load_vec<T, VEC>(x, j, n, G, u);  // (zeros past n: value 0)
     if (quantize_vec<false>(u, s, inv, b)) which |= 1u << min(h, 31);
 #pragma unroll
     for (int p = 0; p < E / 4; ++p) {
@@ -78,6 +88,15 @@ __device__ __forceinline__ float quantize_token(const T* x, int n, int padded, u
           if (j + e * G < padded) xs[j + e * G] = (unsigned char)b[e];
       }
     }
+  };
+#pragma unroll
+  for (int h = 0; h < kTokenHeld; ++h)
+    if (h * G * E < padded) emit(h, v[h]);
+#pragma unroll 2
+  for (int h = kTokenHeld; h * G * E < padded; ++h) {
+    T u[E];
+    load_vec<T, VEC>(x, first_of<T, VEC>(h, tid, G), n, G, u);  // (zeros past n: value 0)
+    emit(h, u);
   }
   if (which || !safe)
     sq += (uint32_t)settle_row<T, VEC>(x, n, tid, G, s, inv, which, (int8_t*)xs);
@@ -89,6 +108,8 @@ __device__ __forceinline__ float quantize_token(const T* x, int n, int padded, u
 // entries are neighbours across the lanes, so weights and activations both
 // come in whole lines (64 codes a lane would spread a warp's activation load
 // over 16 lines).
+// (The loads are volatile: the compiler would move them down to their uses, and
+// with them the time that they take.)
 template <bool CODES>
 struct Weights {
   typedef uint4 type;
@@ -99,6 +120,14 @@ struct Weights<true> {
 };
 constexpr int kEntries = 16, kSpan = 32 * kEntries;
 
+__device__ __forceinline__ void load_weights(uint4& w, const char* p) {
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void load_weights(uint32_t& w, const char* p) {
+  asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w) : "l"(p));
+}
 __device__ __forceinline__ uint32_t four(const uint4& w, int e) { return ((const uint32_t*)&w)[e]; }
 __device__ __forceinline__ uint32_t four(const uint32_t& w, int e) { return (w << (2 * e)) & kCodeMask; }
 
@@ -109,7 +138,7 @@ template <bool CODES, Epilogue EPI, int R, int T, typename RAW, bool VEC>
 __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
   constexpr int P = EPI == kOutFactors ? 2 : 1;  // planes of the activations
   constexpr bool FUSED = sizeof(RAW) > 1;
-  constexpr int U = CODES ? 5 : R == 4 ? 5 : 8;
+  constexpr int U = CODES ? 5 : R == 4 ? 2 : 8;
   typedef typename Weights<CODES>::type W;
   __shared__ uint32_t rowred[FUSED ? 64 : 1];
   extern __shared__ __align__(16) unsigned char xs[];
@@ -129,18 +158,20 @@ __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
       for (int r = 0; r < R; ++r) {
         c[u][r] = W();
         if (at + lane * kEntries < a.K)
-          c[u][r] = __ldg((const W*)(w[r] + at / kEntries * (int)sizeof(W)));
+          load_weights(c[u][r], w[r] + at / kEntries * (int)sizeof(W));
       }
     }
   };
   if (a.early) fetch(0);
   pdl_wait();
   pdl_trigger();
-  if (!a.early) fetch(0);
   float scale = 0.f, z = 0.f;
   if constexpr (FUSED) {
+    RAW v[kTokenHeld][16 / sizeof(RAW)];
+    load_token<RAW, VEC>((const RAW*)a.raw, a.K, v);
+    fetch(0);
     uint32_t squares = 0u;
-    scale = quantize_token<RAW, VEC>((const RAW*)a.raw, a.K, (a.K + 15) / 16 * 16, xs, rowred,
+    scale = quantize_token<RAW, VEC>((const RAW*)a.raw, v, a.K, (a.K + 15) / 16 * 16, xs, rowred,
                                      &squares, EPI == kOutPlanes);
     if (EPI == kOutPlanes)
       z = (float)((double)__ldg(a.rho) * sqrt((double)squares) / kFullScale);
@@ -149,6 +180,8 @@ __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
       if (isnan(scale)) atomicCAS(a.status, 0, EXTERND_ERR_NONFINITE);
     }
     __syncthreads();
+  } else if (!a.early) {
+    fetch(0);
   }
   int acc[R][T][P];
 #pragma unroll
