@@ -27,7 +27,7 @@ constexpr int64_t kPassRows = 4096;
 int64_t type_size(int type) { return type == EXTERND_F32 ? 4 : type == EXTERND_I8 ? 1 : 2; }
 
 int gemm(const GemmArgs& a, Epilogue epi, cudaStream_t st) {
-  if (a.rows <= kTokens) return token_gemm(a, epi, st);
+  if (a.rows == 1) return token_gemm(a, epi, st);
   int dev = 0, nsm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EXTERND_ERR_CUDA;
   cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);

@@ -40,8 +40,7 @@ int launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, in
   return EXTERND_OK;
 }
 
-// The products.
-constexpr int kTokens = 4;          // most rows of token_gemm
+// The products.  token_*: one row; token_raw quantises it itself (GemmArgs::raw).
 constexpr int kTokenInner = 32768;  // longest token that token_raw quantises
 int token_raw(const GemmArgs& a, Epilogue epi, cudaStream_t st);
 int token_gemm(const GemmArgs& a, Epilogue epi, cudaStream_t st);

@@ -1,4 +1,4 @@
-// 8-bit products of a few tokens (single ones above all):
+// 8-bit products of a single token:
 //   dense    y_ti = s_t v_i sum_j q_tj w_ij
 //   planes   h_tc = round(D_c sum_j q_tj C_cj / z_t), as two 8-bit planes
 //   factors  y_ti = s_t z_t sum_c B_ic h_tc
@@ -131,13 +131,13 @@ __device__ __forceinline__ void load_weights(uint32_t& w, const char* p) {
 __device__ __forceinline__ uint32_t four(const uint4& w, int e) { return ((const uint32_t*)&w)[e]; }
 __device__ __forceinline__ uint32_t four(const uint32_t& w, int e) { return (w << (2 * e)) & kCodeMask; }
 
-// T tokens (columns past the last repeat it and are not stored), R rows a
-// warp, U steps of loads in flight.  RAW: the type of a single token that the
+// R rows a warp, U steps of loads in flight.  RAW: the type of a token that the
 // kernel quantises itself (every CTA the whole row: a launch less), or int8_t.
-template <bool CODES, Epilogue EPI, int R, int T, typename RAW, bool VEC>
+// VEC: a token of RAW is read in vectors; an 8-bit one is held in shared memory.
+template <bool CODES, Epilogue EPI, int R, typename RAW, bool VEC>
 __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
   constexpr int P = EPI == kOutFactors ? 2 : 1;  // planes of the activations
-  constexpr bool FUSED = sizeof(RAW) > 1;
+  constexpr bool FUSED = sizeof(RAW) > 1, SHARED = FUSED || VEC;
   constexpr int U = CODES ? 5 : R == 4 ? 2 : 8;
   typedef typename Weights<CODES>::type W;
   __shared__ uint32_t rowred[FUSED ? 64 : 1];
@@ -180,112 +180,125 @@ __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
       if (isnan(scale)) atomicCAS(a.status, 0, EXTERND_ERR_NONFINITE);
     }
     __syncthreads();
+  } else if constexpr (VEC) {
+    // the row (both planes) in shared memory: every warp reads all of it.  Rows
+    // may be padded with anything past K.
+    const int chunks = (a.K + 15) / 16;
+    for (int e = tid; e < P * chunks; e += kTkThreads) {
+      const int p = e >= chunks ? 1 : 0, j = (e - p * chunks) * 16;
+      uint4 v = __ldg((const uint4*)(a.x + p * a.plane + j));
+      if (a.K - j < 16) v = first_bytes(v, a.K - j);
+      *(uint4*)(xs + 16 * e) = v;
+    }
+    if (!a.early) fetch(0);
+    __syncthreads();
   } else if (!a.early) {
     fetch(0);
   }
-  int acc[R][T][P];
+  int acc[R][P];
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int t = 0; t < T; ++t)
-#pragma unroll
-      for (int p = 0; p < P; ++p) acc[r][t][p] = 0;
+    for (int p = 0; p < P; ++p) acc[r][p] = 0;
   for (int k = 0; k < a.K; k += U * kSpan) {
     if (k) fetch(k);
+    uint4 x[U][P];
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const int8_t* xp = FUSED ? nullptr : a.x + (int64_t)min(t, a.rows - 1) * a.ldx;
-      uint4 x[U][P];
+    for (int u = 0; u < U; ++u) {
+      const int kk = k + u * kSpan + lane * kEntries;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int kk = k + u * kSpan + lane * kEntries;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          x[u][p] = make_uint4(0u, 0u, 0u, 0u);
-          if (kk < a.K)
-            x[u][p] = FUSED ? *(const uint4*)(xs + kk) : __ldg((const uint4*)(xp + p * a.plane + kk));
-        }
+      for (int p = 0; p < P; ++p) {
+        x[u][p] = make_uint4(0u, 0u, 0u, 0u);
+        if (kk < a.K)
+          x[u][p] = SHARED ? *(const uint4*)(xs + p * ((a.K + 15) / 16 * 16) + kk)
+                           : __ldg((const uint4*)(a.x + p * a.plane + kk));
       }
-      if (!FUSED && k + U * kSpan > a.K) {  // rows may be padded with anything past K
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int p = 0; p < P; ++p)
-            x[u][p] = first_bytes(x[u][p], a.K - (k + u * kSpan + lane * kEntries));
-      }
+    }
+    if (!SHARED && k + U * kSpan > a.K) {  // the row may be padded with anything past K
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t v = four(c[u][r], e);
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-              acc[r][t][p] = __dp4a((int)v, (int)((const uint32_t*)&x[u][p])[e], acc[r][t][p]);
-          }
+        for (int p = 0; p < P; ++p)
+          x[u][p] = first_bytes(x[u][p], a.K - (k + u * kSpan + lane * kEntries));
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t v = four(c[u][r], e);
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            acc[r][p] = __dp4a((int)v, (int)((const uint32_t*)&x[u][p])[e], acc[r][p]);
+        }
   }
-  // lane r + R t finishes row r of token t
+  // lane r finishes row r
   int sum[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) sum[p] = 0;
 #pragma unroll
-  for (int t = 0; t < T; ++t)
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int v = __reduce_add_sync(0xffffffffu, acc[r][t][p]);
-        if (lane == r + R * t) sum[p] = v;
-      }
-  const int i = i0 + (lane & (R - 1)), t = lane / R;
-  if (t >= T || t >= a.rows || i >= a.M) return;
+    for (int p = 0; p < P; ++p) {
+      const int v = __reduce_add_sync(0xffffffffu, acc[r][p]);
+      if (lane == r) sum[p] = v;
+    }
+  const int i = i0 + lane;
+  if (lane >= R || i >= a.M) return;
   if (CODES) {
 #pragma unroll
     for (int p = 0; p < P; ++p) sum[p] >>= kCodeShift;
   }
   if (EPI == kOutDense) {
-    const float sx = FUSED ? scale : a.xscale[t], v = a.wscale[i] * (float)sum[0];
-    store_out(a.y, (int64_t)t * a.ldy + i, a.ytype, a.bias ? fmaf(sx, v, a.bias[i]) : sx * v);
+    const float sx = FUSED ? scale : a.xscale[0], v = a.wscale[i] * (float)sum[0];
+    store_out(a.y, i, a.ytype, a.bias ? fmaf(sx, v, a.bias[i]) : sx * v);
   } else if (EPI == kOutPlanes) {
-    const int h = component_value(a.wscale[i] * (float)sum[0], FUSED ? z : a.z[t]);
+    const int h = component_value(a.wscale[i] * (float)sum[0], FUSED ? z : a.z[0]);
     const int hi = (h + 128) >> 8;
-    int8_t* y = (int8_t*)a.y + (int64_t)t * a.ldy + i;
+    int8_t* y = (int8_t*)a.y + i;
     y[0] = (int8_t)hi;
     y[a.plane] = (int8_t)(h - 256 * hi);
   } else {
     const float v = fmaf(256.f, (float)sum[0], (float)sum[P - 1]);
-    store_out(a.y, (int64_t)t * a.ldy + i, a.ytype, a.xscale[t] * (a.z[t] * v));
+    store_out(a.y, i, a.ytype, a.xscale[0] * (a.z[0] * v));
   }
 }
 
-template <bool CODES, Epilogue EPI, int R, int T, typename RAW, bool VEC>
+// the token's bytes in shared memory
+template <Epilogue EPI>
+int held_bytes(const GemmArgs& a) {
+  return (a.K + 15) / 16 * 16 * (EPI == kOutFactors ? 2 : 1);
+}
+
+template <bool CODES, Epilogue EPI, int R, typename RAW, bool VEC>
 int launch_r(const GemmArgs& a, cudaStream_t st) {
   constexpr int per = R * kTkThreads / 32;
-  return launch_chained(token_kernel<CODES, EPI, R, T, RAW, VEC>, dim3((unsigned)((a.M + per - 1) / per)),
-                        kTkThreads, sizeof(RAW) > 1 ? (a.K + 15) / 16 * 16 : 0, 0, st, a);
+  return launch_chained(token_kernel<CODES, EPI, R, RAW, VEC>, dim3((unsigned)((a.M + per - 1) / per)),
+                        kTkThreads, sizeof(RAW) > 1 || VEC ? held_bytes<EPI>(a) : 0, 0, st, a);
 }
 
 // More rows a warp reuse a lane's activations; fewer keep all SMs at work.
-template <bool CODES, Epilogue EPI, int T, typename RAW, bool VEC>
+template <bool CODES, Epilogue EPI, typename RAW, bool VEC>
 int launch(const GemmArgs& a, cudaStream_t st) {
-  if (a.M >= 8192) return launch_r<CODES, EPI, 4, T, RAW, VEC>(a, st);
-  if (a.M >= 4096) return launch_r<CODES, EPI, 2, T, RAW, VEC>(a, st);
-  return launch_r<CODES, EPI, 1, T, RAW, VEC>(a, st);
+  if (a.M >= 8192) return launch_r<CODES, EPI, 4, RAW, VEC>(a, st);
+  if (a.M >= 4096) return launch_r<CODES, EPI, 2, RAW, VEC>(a, st);
+  return launch_r<CODES, EPI, 1, RAW, VEC>(a, st);
 }
 
-template <bool CODES, Epilogue EPI>
-int launch_i8(const GemmArgs& a, cudaStream_t st) {
-  if (a.rows == 1) return launch<CODES, EPI, 1, int8_t, true>(a, st);
-  if (a.rows == 2) return launch<CODES, EPI, 2, int8_t, true>(a, st);
-  return launch<CODES, EPI, 4, int8_t, true>(a, st);
+// 8-bit tokens are held in shared memory where the weights are bytes: a warp
+// loads as much of the token as of its row, and over the same path (2560 x 9728:
+// 9.2 us, held 6.5).  Codes are a quarter of that, and the copy's barrier costs
+// more than it saves (the factors of a 2560 x 2560 matrix: 10.0 us, held 11.8).
+int launch_dense(const GemmArgs& a, cudaStream_t st) {
+  return held_bytes<kOutDense>(a) <= 40 * 1024 ? launch<false, kOutDense, int8_t, true>(a, st)
+                                               : launch<false, kOutDense, int8_t, false>(a, st);
 }
 
 template <bool CODES, Epilogue EPI, typename RAW>
 int launch_raw(const GemmArgs& a, cudaStream_t st) {
-  return ((uintptr_t)a.raw & 15) == 0 ? launch<CODES, EPI, 1, RAW, true>(a, st)
-                                      : launch<CODES, EPI, 1, RAW, false>(a, st);
+  return ((uintptr_t)a.raw & 15) == 0 ? launch<CODES, EPI, RAW, true>(a, st)
+                                      : launch<CODES, EPI, RAW, false>(a, st);
 }
 
 template <bool CODES, Epilogue EPI>
@@ -303,9 +316,9 @@ int token_raw(const GemmArgs& a, Epilogue epi, cudaStream_t st) {
 }
 
 int token_gemm(const GemmArgs& a, Epilogue epi, cudaStream_t st) {
-  if (epi == kOutDense) return launch_i8<false, kOutDense>(a, st);
-  if (epi == kOutPlanes) return launch_i8<true, kOutPlanes>(a, st);
-  return launch_i8<true, kOutFactors>(a, st);
+  if (epi == kOutDense) return launch_dense(a, st);
+  if (epi == kOutPlanes) return launch<true, kOutPlanes, int8_t, false>(a, st);
+  return launch<true, kOutFactors, int8_t, false>(a, st);
 }
 
 }  // namespace i8
