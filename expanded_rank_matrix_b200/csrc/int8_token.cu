@@ -278,12 +278,16 @@ int launch_r(const GemmArgs& a, cudaStream_t st) {
                         kTkThreads, sizeof(RAW) > 1 || VEC ? held_bytes<EPI>(a) : 0, 0, st, a);
 }
 
-// More rows a warp reuse a lane's activations; fewer keep all SMs at work.
+// More rows a warp reuse a lane's activations; fewer keep all SMs at work.  The
+// activations weigh four times more against codes than against bytes, so codes
+// take more rows (the factors of a 2560 x 2560 matrix, k 7680: 8.3 us with 4 rows
+// for its components and 2 for its outputs, 8.9 with 2 and 2, 9.9 with 2 and 1,
+// 11.6 with 1 and 1).
 template <bool CODES, Epilogue EPI, typename RAW, bool VEC>
 int launch(const GemmArgs& a, cudaStream_t st) {
-  if (a.M >= 8192) return launch_r<CODES, EPI, 4, RAW, VEC>(a, st);
-  if (a.M >= 4096) return launch_r<CODES, EPI, 2, RAW, VEC>(a, st);
-  return launch_r<CODES, EPI, 1, RAW, VEC>(a, st);
+  if (a.M >= (CODES ? 4096 : 8192)) return launch_r<CODES, EPI, 4, RAW, VEC>(a, st);
+  if (CODES || a.M >= 4096) return launch_r<CODES, EPI, 2, RAW, VEC>(a, st);
+  return launch_r<false, kOutDense, 1, RAW, VEC>(a, st);
 }
 
 // 8-bit tokens are held in shared memory where the weights are bytes: a warp
