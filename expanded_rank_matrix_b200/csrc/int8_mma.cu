@@ -112,34 +112,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
   const uint32_t tmem = tmem_base;
   if (a.early) pdl_trigger();
 
+  auto weights = [&](int s, int k, int wrow) {
+    const uint32_t dst = smem_u32(ring + s * kStageBytes), bar = smem_u32(&bars.full[s]);
+    if (rank == 0) bar_expect(bar, 2u * (uint32_t)((CODES ? 0 : kOperand) + half * kKStep));
+    if (CODES) {
+      const uint32_t cbar = smem_u32(&bars.codes[s]);
+      bar_expect(cbar, kCodeBytes);
+      tma_2d_own(dst + 2 * kOperand, &wmap, k * kCodeRow, wrow, cbar);
+    } else {
+      tma_2d(dst, &wmap, k * kKStep, wrow, in_leader(bar));
+    }
+  };
+  auto tokens = [&](int s, int k, int tt) {
+    tma_3d(smem_u32(ring + s * kStageBytes) + kOperand, &xmap, k * kKStep,
+           EPI == kOutFactors ? tt * per : tt * per + rank * half,
+           EPI == kOutFactors ? rank : 0, in_leader(smem_u32(&bars.full[s])));
+  };
+
   if (wid == 0) {
     if (elect_one()) {  // ---- TMA producer ----
-      const uint32_t tx = 2u * (uint32_t)((CODES ? 0 : kOperand) + half * kKStep);
-      auto weights = [&](int s, int k, int wrow) {
-        const uint32_t dst = smem_u32(ring + s * kStageBytes), bar = smem_u32(&bars.full[s]);
-        if (rank == 0) bar_expect(bar, tx);
-        if (CODES) {
-          const uint32_t cbar = smem_u32(&bars.codes[s]);
-          bar_expect(cbar, kCodeBytes);
-          tma_2d_own(dst + 2 * kOperand, &wmap, k * kCodeRow, wrow, cbar);
-        } else {
-          tma_2d(dst, &wmap, k * kKStep, wrow, in_leader(bar));
-        }
-      };
-      auto tokens = [&](int s, int k, int tt) {
-        tma_3d(smem_u32(ring + s * kStageBytes) + kOperand, &xmap, k * kKStep,
-               EPI == kOutFactors ? tt * per : tt * per + rank * half,
-               EPI == kOutFactors ? rank : 0, in_leader(smem_u32(&bars.full[s])));
-      };
       if (!a.early) {
         pdl_wait();
         pdl_trigger();
       }
-      const int ahead = pair < tiles ? min(kStages, ksteps) : 0;
+      // Codes and activations have one producer: codes come first, they have
+      // the unpacking before them (with two, the factors of 201 x 1533 x 1000,
+      // k 2001, took 15.9 us for 15.5).
+      const int ahead = CODES && pair < tiles ? min(kStages, ksteps) : 0;
       const int wrow0 = (pair % MT) * 256 + rank * kHalfRows;
-      for (int k = 0; k < ahead; ++k) weights(k, k, wrow0);
-      pdl_wait();
-      for (int k = 0; k < ahead; ++k) tokens(k, k, pair / MT);
+      if (CODES) {
+        for (int k = 0; k < ahead; ++k) weights(k, k, wrow0);
+        pdl_wait();
+        for (int k = 0; k < ahead; ++k) tokens(k, k, pair / MT);
+      }
       int i = ahead;
       bool ok = true;
       for (int tile = pair; tile < tiles && ok; tile += npairs) {
@@ -152,6 +157,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
             break;
           }
           weights(s, k, wrow);
+          if (CODES) tokens(s, k, tt);
+        }
+      }
+    }
+  } else if (!CODES && wid == 3) {
+    // 8-bit weights and the activations have a producer each: one for both was
+    // still issuing the first ring's activations 0.5 us after its weights
+    // (333 x 1371 x 2001 product: 9.3 us for 8.8).
+    if (elect_one()) {
+      pdl_wait();
+      int i = 0;
+      bool ok = true;
+      for (int tile = pair; tile < tiles && ok; tile += npairs) {
+        const int tt = tile / MT;
+        for (int k = 0; k < ksteps; ++k, ++i) {
+          const int s = i % kStages;
+          if (i >= kStages &&
+              !bar_wait(smem_u32(&bars.empty[s]), ((i / kStages) + 1) & 1, ab, a.budget)) {
+            ok = false;
+            break;
+          }
           tokens(s, k, tt);
         }
       }
@@ -316,13 +342,15 @@ int launch(const GemmArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Estimated time in units of 10 ns, fitted over the shapes of split_plan's
-// (2560 x 2560: 7.0 us at 16 tokens, 7.5 at 256, 10.0 at 1000; 2560 x 9728: 16.2,
-// 18.7, 22.1).  The split kernel is taken where its estimate is below this.
+// Estimated time in units of 10 ns, fitted over the shapes of split_plan's (8-bit
+// operands, 2560 x 2560: 5.5 us at 16 tokens, 6.4 at 256, 7.7 at 700; 2560 x 9728:
+// 17.5, 17.2, 18.7).  The split kernel is taken where its estimate is below this:
+// over 2 .. 700 tokens of seven shapes the one taken was the slower one in four of
+// 98 cases, by at most 15 %.
 long long mma_cost(const GemmArgs& a, Epilogue epi, int nsm) {
   const PairPlan p = pair_plan(a, epi, nsm);
-  const int step = epi == kOutDense ? 13 + p.NT * 6 / 100 : 19 + p.NT * 4 / 100;
-  return 430 + p.rounds * ((a.K + kKStep - 1) / kKStep) * step;
+  const int step = epi == kOutDense ? 14 + p.NT * 6 / 100 : 19 + p.NT * 4 / 100;
+  return (epi == kOutDense ? 385 : 430) + p.rounds * ((a.K + kKStep - 1) / kKStep) * step;
 }
 
 int mma_gemm(const GemmArgs& a, Epilogue epi, cudaStream_t st) {
