@@ -54,6 +54,7 @@ constexpr int kStages = 6;
 constexpr int kStageBytes = 2 * kOperand + kCodeBytes;
 constexpr int kAccCols = 256;               // tensor-memory columns of an accumulator
 constexpr int kUnpackWarp0 = 4, kUnpackGroups = 2, kEpiWarps = 8;
+static_assert(kStages % kUnpackGroups == 0, "a stage comes to the same group each time round");
 constexpr int epi_warp0(bool codes) { return kUnpackWarp0 + (codes ? 4 * kUnpackGroups : 0); }
 constexpr int mma_threads(bool codes) { return 32 * (epi_warp0(codes) + kEpiWarps); }
 constexpr int kMmaSmem = kStages * kStageBytes + 1024;

@@ -38,9 +38,37 @@ namespace {
 
 constexpr int kMaxStages = 8, kMaxSplit = 8;
 constexpr int kSplitThreads = 384, kFinishWarp0 = 4, kFinishWarps = 8;
+constexpr int kUnpackGroups = 2;
 constexpr int kSplitSmemMax = 222 * 1024;  // (the scales and barriers take the rest)
 // at least this much, so that no two CTAs of these kernels share an SM
 constexpr int kSplitSmemMin = 116 * 1024;
+
+// Bytes of a stage (weights, activations, packed codes), of the sums of the
+// tokens that a CTA owns, and the stages that fit beside them.  With codes they
+// are a multiple of the unpacking groups: the groups take turns, and a stage has
+// to come to the same group each time round.  A group that met another's stage
+// could wait for the second landing there before the first, which a wait by
+// parity lets through at once.
+constexpr int stage_bytes_of(int NT, bool codes) {
+  return kOperand + NT * kKStep + (codes ? kCodeBytes : 0);
+}
+constexpr int sums_bytes_of(int per, int P, int S) { return (per + S - 1) / S * P * 512; }
+constexpr int stages_of(int NT, int P, int S, bool codes) {
+  const int room = kSplitSmemMax - 1024 - sums_bytes_of(NT / P, P, S);
+  const int fit = room / stage_bytes_of(NT, codes);
+  const int n = fit < kMaxStages ? fit : kMaxStages;
+  return codes ? n / kUnpackGroups * kUnpackGroups : n;
+}
+constexpr bool rings_hold() {
+  for (int P = 1; P <= 2; ++P)
+    for (int S = 1; S <= kMaxSplit; ++S)
+      for (int NT = 16; NT <= (S == 1 ? 64 : 256); NT += 16)
+        if (stages_of(NT, P, S, false) < 2 || stages_of(NT, P, S, true) < 2 ||
+            stages_of(NT, P, S, true) % kUnpackGroups != 0)
+          return false;
+  return true;
+}
+static_assert(rings_hold(), "every split has a ring, and a stage one unpacking group");
 
 struct SplitBars {
   uint64_t full[kMaxStages], empty[kMaxStages], codes[kMaxStages], accf, sums, drain;
@@ -144,7 +172,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   constexpr int P = EPI == kOutFactors ? 2 : 1;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  int* sums = (int*)(ring + stages * (kOperand + NT * kKStep + (CODES ? kCodeBytes : 0)));
+  int* sums = (int*)(ring + stages * stage_bytes_of(NT, CODES));
   __shared__ __align__(8) SplitBars bars;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
@@ -154,7 +182,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const int ksteps = (a.K + kKStep - 1) / kKStep;
   const int k0 = rank * ksteps / S, steps = (rank + 1) * ksteps / S - k0;
   const int xbytes = NT * kKStep;
-  const int stage_bytes = kOperand + xbytes + (CODES ? kCodeBytes : 0);
+  const int stage_bytes = stage_bytes_of(NT, CODES);
   const uint32_t tcols = NT <= 32 ? 32u : NT <= 64 ? 64u : NT <= 128 ? 128u : 256u;
   volatile int* ab = &abort_flag;
   // the CTA's tokens: every S-th of the tile's, [token][plane][row] in `sums`
@@ -261,7 +289,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     if (CODES) {  // ---- codes: a row a thread, the two groups on alternate steps ----
       const int row = quad * 32 + lane;
       // (a stage's codes land after its last MMAs are done: the operand is free)
-      for (int i = half; i < steps; i += 2) {
+      for (int i = half; i < steps; i += kUnpackGroups) {
         const int s = i % stages;
         const bool got = bar_wait(smem_u32(&bars.codes[s]), (i / stages) & 1, ab, a.budget);
         if (!__all_sync(0xffffffffu, got)) break;
@@ -372,10 +400,9 @@ int launch(const GemmArgs& a, const SplitPlan& p, cudaStream_t st) {
       !(CODES ? byte_map(&wmap, a.w, 4 * a.ldw, a.M, 4 * a.ldw, 0, 0, kCodeRow, kHalfRows)
               : byte_map(&wmap, a.w, a.K, a.M, a.ldw, 0, 0, kKStep, kHalfRows)))
     return EXTERND_ERR_CUDA;
-  const int stage_bytes = kOperand + NT * kKStep + (CODES ? kCodeBytes : 0);
-  const int sums = (p.per + p.S - 1) / p.S * P * 512;
-  const int stages = std::min(kMaxStages, (kSplitSmemMax - 1024 - sums) / stage_bytes);
-  const int smem = std::max(stages * stage_bytes + sums + 1024, kSplitSmemMin);
+  const int stages = stages_of(NT, P, p.S, CODES);
+  const int smem = std::max(
+      stages * stage_bytes_of(NT, CODES) + sums_bytes_of(p.per, P, p.S) + 1024, kSplitSmemMin);
   return launch_chained(split_kernel<CODES, EPI>, dim3((unsigned)(p.MT * p.S), (unsigned)p.TT),
                         kSplitThreads, smem, p.S, st, xmap, wmap, a, NT, p.S, stages);
 }

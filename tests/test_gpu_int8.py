@@ -388,6 +388,30 @@ def test_apply_long_prompts(t):
     R.check(y, *R.factors(*R.rows(x), B, C, D))
 
 
+@pytest.mark.parametrize("t", [33, 48, 64, 80, 100, 128, 160, 250])
+def test_apply_split_over_long_dimensions(t):
+    """Many steps of codes through rings of every depth (a ring's depth follows
+    the tokens), beside copies on another stream that delay their arrivals."""
+    m, n, k = 512, 8192, 384
+    f, B, C, D = _factors(m, n, k, t)
+    f2, B2, C2, D2 = _factors(k, 512, 8192, t + 1)
+    x, x2 = _x(t, n, torch.bfloat16, t), _x(t, 512, torch.bfloat16, t)
+    c, c2 = X.pack_codes(f), X.pack_codes(f2)
+    R.check(X.apply_i8(c, x, out_dtype=torch.float32), *R.factors(*R.rows(x), B, C, D))
+    R.check(X.apply_i8(c2, x2, out_dtype=torch.float32), *R.factors(*R.rows(x2), B2, C2, D2))
+    first = X.apply_i8(c, x), X.apply_i8(c2, x2)
+    a, b = torch.ones(1 << 26, device="cuda"), torch.empty(1 << 26, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(40):
+            b.copy_(a)
+    again = [(X.apply_i8(c, x), X.apply_i8(c2, x2)) for _ in range(60)]
+    torch.cuda.synchronize()
+    for y, y2 in again:
+        assert torch.equal(y, first[0]) and torch.equal(y2, first[1])
+
+
 def test_many_rows_of_a_narrow_product():
     """More rows than one pass of the dense product quantises, and 64-bit
     offsets in the output."""
