@@ -11,20 +11,33 @@
 // one CTA of the pair holds plane hi, the other plane lo, and the unpacked
 // codes serve both.
 //
-// The K loop runs in steps of 128 bytes through a ring of shared-memory
-// stages (128-byte swizzled rows).  Activations and 8-bit weights arrive by
+// The K loop runs in steps of 128 bytes through a ring of six and more
+// shared-memory stages (128-byte swizzled rows).  Activations and 8-bit weights arrive by
 // TMA, which fills zeros past K, the last row and the last token.  Two-bit
-// codes arrive by TMA too (4 KB a step) and two groups of four warps unpack them, a row a
-// thread, two instructions for four codes, into the signed bytes +-64 the
-// tensor core reads.  (With the codes loaded into the unpacking warps' own
-// registers four steps ahead, a step took about 1800 cycles: the arrival on the
-// even CTA's barrier is a release that waits for the warp's loads in flight.)  Accumulators
-// double up in tensor memory, so the epilogue of a tile runs beside the K
-// loop of the next one.
+// codes arrive by TMA too (4 KB a step; five stages with codes of four steps
+// each were slower) and two groups of four warps unpack them, a row a thread,
+// two instructions for four codes, into the signed bytes +-64 the tensor core
+// reads.  Accumulators double up in tensor memory, so the epilogue of a tile
+// runs beside the K loop of the next one.
+//
+// Bounds.  8-bit operands: the tensor cores; 8192 x 9728 x 2560 takes 125 us
+// alone (3.27 P operations a second, against 3.33 P for twice the measured
+// 16-bit rate), and 168 us run without a pause, where the power limit holds the
+// clock (2.43 P, against 2.79 P).  Codes: the shared-memory pipe beside them; a
+// step of a 256-column tile moves the unpacked codes in and both operands out,
+// about 576 cycles of that pipe for 512 of products.  Narrow tiles: a step takes
+// about 350 cycles however few its columns are (2560 x 9728 at 16 to 512 tokens:
+// 17.2 .. 17.7 us).  More stages, codes in contiguous blocks, a third producer and
+// codes read ahead of the fence all left that as it is, which points at the
+// matrix instructions, each reading its whole weight operand.
+// 4096 x 2560 x 2560, k 7680: 72 us the component sums, whose epilogue rounds 31
+// million of them, 94 us the second half with its two planes, 148 us in all, the
+// second half's start overlapping the first's end.
 //
 // Warp roles (per CTA): 0 TMA producer, 1 MMA issuer (even CTA of the pair),
-// 2 tensor-memory allocation, then (codes only) two groups of four that unpack
-// alternate steps, and eight for the epilogue.
+// 2 tensor-memory allocation, 3 TMA producer of the activations (8-bit weights
+// only), then (codes only) two groups of four that unpack alternate steps, and
+// eight for the epilogue.
 // mbarriers: full (even CTA: both CTAs' copies and unpacked codes of a stage),
 // codes (each CTA: a stage's packed codes have landed),
 // empty (each CTA: the stage's MMAs are done), accf / accfree (an accumulator
@@ -49,26 +62,38 @@ namespace externd {
 namespace i8 {
 namespace {
 
-constexpr int kStages = 6;
+constexpr int kMaxStages = 12;
+constexpr int kRingBytes = 220 * 1024;
 // weights, activations, packed codes (only where the weights are codes)
-constexpr int kStageBytes = 2 * kOperand + kCodeBytes;
+constexpr int stage_bytes_of(int NT, bool codes) {
+  return kOperand + NT / 2 * kKStep + (codes ? kCodeBytes : 0);
+}
 constexpr int kAccCols = 256;               // tensor-memory columns of an accumulator
 constexpr int kUnpackWarp0 = 4, kUnpackGroups = 2, kEpiWarps = 8;
-static_assert(kStages % kUnpackGroups == 0, "a stage comes to the same group each time round");
+// The stages that fit.  With codes they are a multiple of the unpacking groups,
+// so that a stage comes to the same group each time round: a group that met
+// another's could wait for the second landing of codes there before the first,
+// which a wait by parity lets through at once.
+constexpr int stages_of(int NT, bool codes) {
+  const int fit = kRingBytes / stage_bytes_of(NT, codes);
+  const int n = fit < kMaxStages ? fit : kMaxStages;
+  return codes ? n / kUnpackGroups * kUnpackGroups : n;
+}
 constexpr int epi_warp0(bool codes) { return kUnpackWarp0 + (codes ? 4 * kUnpackGroups : 0); }
 constexpr int mma_threads(bool codes) { return 32 * (epi_warp0(codes) + kEpiWarps); }
-constexpr int kMmaSmem = kStages * kStageBytes + 1024;
+constexpr int kMmaSmem = kRingBytes + 1024;
 static_assert(2 * kMmaSmem > 228 * 1024, "one CTA per SM: it takes all of tensor memory");
+static_assert(stages_of(256, true) >= kUnpackGroups && stages_of(256, false) >= 2, "a ring");
 
 struct Bars {
-  uint64_t full[kStages], empty[kStages], codes[kStages], accf[2], accfree[2], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], codes[kMaxStages], accf[2], accfree[2], drain;
 };
 
 // MT tiles of 256 weight rows, TT tiles of NT tokens (kOutFactors: NT / 2).
 template <bool CODES, Epilogue EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 1)
     mma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-               const GemmArgs a, int NT, int MT, int TT) {
+               const GemmArgs a, int NT, int MT, int TT, int stages) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ __align__(8) Bars bars;
@@ -83,6 +108,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
   const int per = EPI == kOutFactors ? half : NT;  // tokens a tile covers
   const int ksteps = (a.K + kKStep - 1) / kKStep;
   const int tiles = MT * TT;
+  const int stage_bytes = stage_bytes_of(NT, CODES);
   volatile int* ab = &abort_flag;
 
   if (wid == 2) {
@@ -93,7 +119,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       bar_init(smem_u32(&bars.full[s]), CODES ? 9 : 1);
       bar_init(smem_u32(&bars.empty[s]), 1);
       bar_init(smem_u32(&bars.codes[s]), 1);
@@ -114,18 +140,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
   if (a.early) pdl_trigger();
 
   auto weights = [&](int s, int k, int wrow) {
-    const uint32_t dst = smem_u32(ring + s * kStageBytes), bar = smem_u32(&bars.full[s]);
+    const uint32_t dst = smem_u32(ring + s * stage_bytes), bar = smem_u32(&bars.full[s]);
     if (rank == 0) bar_expect(bar, 2u * (uint32_t)((CODES ? 0 : kOperand) + half * kKStep));
     if (CODES) {
       const uint32_t cbar = smem_u32(&bars.codes[s]);
       bar_expect(cbar, kCodeBytes);
-      tma_2d_own(dst + 2 * kOperand, &wmap, k * kCodeRow, wrow, cbar);
+      tma_2d_own(dst + stage_bytes - kCodeBytes, &wmap, k * kCodeRow, wrow, cbar);
     } else {
       tma_2d(dst, &wmap, k * kKStep, wrow, in_leader(bar));
     }
   };
   auto tokens = [&](int s, int k, int tt) {
-    tma_3d(smem_u32(ring + s * kStageBytes) + kOperand, &xmap, k * kKStep,
+    tma_3d(smem_u32(ring + s * stage_bytes) + kOperand, &xmap, k * kKStep,
            EPI == kOutFactors ? tt * per : tt * per + rank * half,
            EPI == kOutFactors ? rank : 0, in_leader(smem_u32(&bars.full[s])));
   };
@@ -139,26 +165,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
       // Codes and activations have one producer: codes come first, they have
       // the unpacking before them (with two, the factors of 201 x 1533 x 1000,
       // k 2001, took 15.9 us for 15.5).
-      const int ahead = CODES && pair < tiles ? min(kStages, ksteps) : 0;
+      const int ahead = CODES && pair < tiles ? min(stages, ksteps) : 0;
       const int wrow0 = (pair % MT) * 256 + rank * kHalfRows;
       if (CODES) {
         for (int k = 0; k < ahead; ++k) weights(k, k, wrow0);
         pdl_wait();
         for (int k = 0; k < ahead; ++k) tokens(k, k, pair / MT);
       }
-      int i = ahead;
+      int s = ahead == stages ? 0 : ahead, phase = ahead == stages ? 0 : 1;
       bool ok = true;
       for (int tile = pair; tile < tiles && ok; tile += npairs) {
         const int wrow = (tile % MT) * 256 + rank * kHalfRows, tt = tile / MT;
-        for (int k = tile == pair ? ahead : 0; k < ksteps; ++k, ++i) {
-          const int s = i % kStages;
-          if (i >= kStages &&
-              !bar_wait(smem_u32(&bars.empty[s]), ((i / kStages) + 1) & 1, ab, a.budget)) {
+        for (int k = tile == pair ? ahead : 0; k < ksteps; ++k) {
+          if (!bar_wait(smem_u32(&bars.empty[s]), phase, ab, a.budget)) {
             ok = false;
             break;
           }
           weights(s, k, wrow);
           if (CODES) tokens(s, k, tt);
+          if (++s == stages) s = 0, phase ^= 1;
         }
       }
     }
@@ -168,18 +193,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     // (333 x 1371 x 2001 product: 9.3 us for 8.8).
     if (elect_one()) {
       pdl_wait();
-      int i = 0;
+      int s = 0, phase = 1;
       bool ok = true;
       for (int tile = pair; tile < tiles && ok; tile += npairs) {
         const int tt = tile / MT;
-        for (int k = 0; k < ksteps; ++k, ++i) {
-          const int s = i % kStages;
-          if (i >= kStages &&
-              !bar_wait(smem_u32(&bars.empty[s]), ((i / kStages) + 1) & 1, ab, a.budget)) {
+        for (int k = 0; k < ksteps; ++k) {
+          if (!bar_wait(smem_u32(&bars.empty[s]), phase, ab, a.budget)) {
             ok = false;
             break;
           }
           tokens(s, k, tt);
+          if (++s == stages) s = 0, phase ^= 1;
         }
       }
     }
@@ -200,8 +224,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
             ok = false;
             break;
           }
-          const uint32_t at = base + s * kStageBytes, done = smem_u32(&bars.empty[s]);
-          if (++s == kStages) s = 0, phase ^= 1;
+          const uint32_t at = base + s * stage_bytes, done = smem_u32(&bars.empty[s]);
+          if (++s == stages) s = 0, phase ^= 1;
           ready = bar_peek(smem_u32(&bars.full[s]), phase);  // (the next step's)
           mma_step<true>(acc + q * kAccCols, operand_desc(at), operand_desc(at + kOperand), idesc,
                          k > 0, done);
@@ -218,15 +242,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     // (a stage's codes land after its last MMAs are done: the operand is free)
     const int row = (wid & 3) * 32 + lane;
     const int mine = pair < tiles ? (tiles - pair + npairs - 1) / npairs * ksteps : 0;
-    for (int i = (wid - kUnpackWarp0) >> 2; i < mine; i += kUnpackGroups) {
-      const int s = i % kStages;
-      const bool got = bar_wait(smem_u32(&bars.codes[s]), (i / kStages) & 1, ab, a.budget);
+    int s = (wid - kUnpackWarp0) >> 2, phase = 0;
+    for (int i = s; i < mine; i += kUnpackGroups) {
+      const bool got = bar_wait(smem_u32(&bars.codes[s]), phase, ab, a.budget);
       if (!__all_sync(0xffffffffu, got)) break;
-      unsigned char* stage = ring + s * kStageBytes;
-      unpack_row(stage + 2 * kOperand, stage, row);
+      unsigned char* stage = ring + s * stage_bytes;
+      unpack_row(stage + stage_bytes - kCodeBytes, stage, row);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) bar_arrive_cluster(in_leader(smem_u32(&bars.full[s])));
+      if ((s += kUnpackGroups) >= stages) s -= stages, phase ^= 1;
     }
   } else if (wid >= kEpiWarp0) {
     // ---- epilogue: warp w reads lanes 32 (w % 4) .., one half of the columns ----
@@ -338,7 +363,8 @@ int launch(const GemmArgs& a, cudaStream_t st) {
     return EXTERND_ERR_CUDA;
   return launch_chained(mma_kernel<CODES, EPI>,
                         dim3(2u * (unsigned)std::min<long long>(pairs, MT * TT)), mma_threads(CODES),
-                        kMmaSmem, 0, st, xmap, wmap, a, NT, MT, (int)TT);
+                        kMmaSmem, 0, st, xmap, wmap, a, NT, MT, (int)TT,
+                        stages_of(NT, CODES));
 }
 
 }  // namespace

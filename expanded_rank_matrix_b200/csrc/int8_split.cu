@@ -6,7 +6,7 @@
 // (tokens, or the two planes of NT / 2 tokens), each CTA a run of the K steps:
 // the weights' bytes, which bound these products, stream through S times as
 // many SMs.  Every token of the tile has an owner among the CTAs, and each CTA
-// adds its whole-number sums of the token into the owner's shared memory by
+// adds its whole-number sums of the token to the owner's shared memory by
 // asynchronous remote additions that count on the owner's barrier; when all
 // have come, the owner finishes its tokens.  Nothing waits on a round trip, and
 // no cluster barrier stands in the way.  (Peers reading one another's sums
@@ -14,6 +14,12 @@
 // sums are exact in any order, so the split does not show in the results.
 // The weights of the first ring fill are requested before the kernel waits
 // for the one in front of it.
+//
+// 32 x 2560 x 9728 on 8-bit operands (25.4 MB): 6.5 us, 60 % of the measured
+// copy rate; about 2.5 us of it is the kernel's start and the sums' way to their
+// owners, which small products are all of (32 x 1024 x 1024: 3.6 us).  Among
+// the splits whose clusters the GPU holds at once, the one of the fewest steps
+// is taken.
 //
 // Warp roles: 0 TMA producer, 1 MMA issuer, 2 tensor-memory allocation, 4..11
 // unpack codes (two groups of four, alternate steps), then read the

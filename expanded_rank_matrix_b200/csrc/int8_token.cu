@@ -4,14 +4,20 @@
 //   factors  y_ti = s_t z_t sum_c B_ic h_tc
 // Bound by the weights' bytes, and for a single projection by latency: what
 // counts is that every load is on its way at once.  A warp takes R weight rows
-// and its lanes the inner dimension, 16 bytes of a row each (16 8-bit weights,
-// or 64 codes, which unpack in two instructions for four); the products are
+// and its lanes the inner dimension, 16 weights of a row each (16 bytes, or one
+// word of 16 codes, which unpack in two instructions for four); the products are
 // four-way 8-bit dot products, and a row's 32 partial sums are added by one
-// warp-wide whole-number reduction, so no barrier is needed.  The first
-// weights are requested before the kernel waits for the one in front of it,
-// or quantises its token.
-// (Warp-level 16 x 8 x 32 matrix instructions in their place fill eight columns
-// for one token and took 2.3 us of a 2560 x 7680 factor's product alone.)
+// warp-wide whole-number reduction.  The only barriers are those behind the
+// token, where a CTA quantises it or holds it in shared memory.  The token is
+// requested before any weights, behind which it would wait (9728 x 2560: 7.4 us,
+// 5.4 this way), and the first weights before the kernel waits for the one in
+// front of it, or quantises its token.
+//
+// 9728 x 2560 (24.9 MB): 5.4 us, 70 % of the measured copy rate; 2560 x 9728:
+// 6.5 us.  Factors of 2560 x 2560, k 7680 (9.8 MB of codes): 8.4 us for both
+// halves, of which 1.5 us would be their bytes: two kernels' starts, and the
+// unpacking.  (Warp-level matrix instructions in place of the dot products fill
+// eight columns for one token: 18.4 us for 10.5 at the same stage.)
 
 #include <cuda_runtime.h>
 

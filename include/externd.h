@@ -306,7 +306,8 @@ int externd_quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, in
  *
  *   X       [rows][ldx] of xtype.  EXTERND_F32 / _F16 / _BF16: quantised within the call as
  *           externd_quantize_rows does (scratch: rows * (n + 19) bytes at most, for at
- *           most 65536 rows at a time); xscale is ignored.  EXTERND_I8:
+ *           most 65536 rows at a time; none for one row), rows that are not
+ *           finite as there; xscale is ignored.  EXTERND_I8:
  *           q itself, 16-byte aligned, ldx a multiple of 16 (every row, the
  *           last one too, holds ldx readable bytes; those past n do not
  *           count), with xscale [rows].
@@ -360,8 +361,8 @@ int externd_pack_codes(const uint32_t* packed_B, const uint32_t* packed_C, const
  * batched.  The fixed scale z_t costs log2(sqrt(n)) of h's bits against a
  * scale from the true maximum, and saves the pass over all sums that would
  * find it; what is left (a step of z_t) is below the step of the 8-bit
- * activations.  fp32 arithmetic, rounded once to ytype.  A component with a
- * NaN or infinite D makes every result NaN or 0 * infinity.
+ * activations.  fp32 arithmetic, rounded once to ytype.  A NaN or an infinity in
+ * D makes the bound one, and every result NaN.
  *
  *   codes_B, codes_C, bound: from externd_pack_codes; D [k] the same as there.
  *   X, xtype, ldx, xscale, rows, Y, ytype, ldy: as for externd_matmul_i8.
