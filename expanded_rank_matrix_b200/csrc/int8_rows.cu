@@ -5,9 +5,9 @@
 // to x_j / s (exact, ties to even).  One pass: a group of threads holds its
 // row in registers between the maximum and the rounding, so the row is read
 // once and its 8-bit copy written once; HBM bandwidth is the bound (8192 x 9728
-// bf16: 44.6 us, 82 % of the measured copy rate; 8192 x 2560: 12.4 us; 4099 x
-// 2559 fp32, whose rows are not aligned and are read an element at a time, 12.5
-// us, 64 %).  A launch of a single row is 1.6 us behind another.
+// bf16: 39.9 us, 92 % of the measured copy rate; 8192 x 2560: 12.0 us; 4099 x
+// 2559 fp32, whose rows are not aligned and are read an element at a time, 12.0
+// us, 67 %).  A launch of a single row is 1.6 us behind another.
 
 #include <cuda_runtime.h>
 
@@ -39,10 +39,19 @@ struct RowArgs {
 };
 
 constexpr int kWarpRows = 8;  // rows of a CTA where a warp takes a row
+// Registers of a thread.  Fewer than the compiler would take (56): the rows that
+// an SM holds at once carry the bandwidth, which is worth the odd spill (8192 x
+// 9728 bf16: 39.9 us for 44.6, fp32 rows of 9728 33.9 for 40.6).  The 16-bit
+// rows of a warp each, or read by elements, spill too much (8192 x 1000: 7.2 us
+// for 5.9; 4099 x 2559: 16.2 for 11.0) and keep theirs.
+template <typename T>
+constexpr int row_regs(bool vec, bool warp) {
+  return sizeof(T) == 4 ? (vec ? 40 : 48) : vec && !warp ? 40 : 64;
+}
 
 // A warp (WARP) or a CTA takes a row; a thread holds H 16-byte vectors of it.
 template <typename T, int H, bool VEC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rows_kernel(const RowArgs<T> a) {
+__global__ void __maxnreg__((row_regs<T>(VEC, WARP))) rows_kernel(const RowArgs<T> a) {
   constexpr int E = 16 / sizeof(T);
   __shared__ uint32_t red[2][32];
   pdl_wait();
@@ -164,11 +173,12 @@ int launch_rows_h(const RowArgs<T>& a, int threads, cudaStream_t st) {
                         dim3((unsigned)grid), threads, 0, 0, st, a);
 }
 
-// HBM stays busy through the bytes in flight on an SM and many small CTAs
-// whose load, reduction and store phases overlap.  Five vectors a thread were
-// best wherever there are rows enough (8192 x 9728 bf16: 51 us, against 178,
-// 109, 71, 58, 54 and 65 us with 1, 2, 3, 4, 6 and 8; 2048 x 9728 fp32: 24 us
-// against 25 .. 50); a few rows take two, as the time of one row counts.
+// HBM stays busy through the rows in flight on an SM: many small CTAs whose
+// load, reduction and store phases overlap.  Five vectors a thread were best
+// wherever there are rows enough (8192 x 9728 bf16: 39.9 us, against 49.7, 44.3 and
+// 41.5 us with 3, 4 and 6), unless the longer rows' CTAs then leave an SM half
+// empty (2048 x 32768 bf16: 50.3 us, with 6, where two of them fit, 39.0); a few
+// rows take two, as the time of one row counts.
 template <typename T>
 int launch_rows(const RowArgs<T>& a, cudaStream_t st) {
   const int vecs = (int)((a.n * (int64_t)sizeof(T) + 15) / 16);
@@ -178,6 +188,8 @@ int launch_rows(const RowArgs<T>& a, cudaStream_t st) {
     if (vecs <= 1024 * 2) return launch_rows_h<T, 2, false>(a, threads(2), st);
   }
   if (vecs <= 32 * 5) return launch_rows_h<T, 5, true>(a, 32 * kWarpRows, st);
+  auto held = [&](int h) { return 65536 / (row_regs<T>(true, false) * threads(h)); };  // rows of an SM
+  if (2 * held(6) >= 3 * held(5)) return launch_rows_h<T, 6, false>(a, threads(6), st);
   return launch_rows_h<T, 5, false>(a, threads(5), st);
 }
 
