@@ -137,7 +137,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
   cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_base;
-  if (a.early) pdl_trigger();
+  // (no bounded wait starts before the work in front is done, however long that
+  // takes; where it is of the same call, it has itself waited for the rest)
+  if (!a.early) pdl_wait();
+  pdl_trigger();
 
   auto weights = [&](int s, int k, int wrow) {
     const uint32_t dst = smem_u32(ring + s * stage_bytes), bar = smem_u32(&bars.full[s]);
@@ -158,10 +161,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
 
   if (wid == 0) {
     if (elect_one()) {  // ---- TMA producer ----
-      if (!a.early) {
-        pdl_wait();
-        pdl_trigger();
-      }
       // Codes and activations have one producer: codes come first, they have
       // the unpacking before them (with two, the factors of 201 x 1533 x 1000,
       // k 2001, took 15.9 us for 15.5).

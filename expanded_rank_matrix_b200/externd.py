@@ -411,7 +411,7 @@ def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=No
     each token and each output channel (externd_matmul_i8).  X: [..., n] fp32,
     fp16 or bf16, quantised within the call, or Quantized rows (shared by
     several products).  The output is [..., m] of out_dtype (default: X's
-    type; fp32 for Quantized)."""
+    type; fp32 for Quantized).  Not differentiable: no gradient reaches X."""
     if stream is not None:
         with _elsewhere(W.q.get_device(), stream):
             return matmul_i8(X, W, bias, out_dtype)
