@@ -64,11 +64,22 @@ namespace {
 
 constexpr int kMaxStages = 12;
 constexpr int kRingBytes = 220 * 1024;
-// weights, activations, packed codes (only where the weights are codes)
+// activations, and 8-bit weights or packed codes
 constexpr int stage_bytes_of(int NT, bool codes) {
-  return kOperand + NT / 2 * kKStep + (codes ? kCodeBytes : 0);
+  return NT / 2 * kKStep + (codes ? kCodeBytes : kOperand);
 }
-constexpr int kAccCols = 256;               // tensor-memory columns of an accumulator
+constexpr int kAccCols = 256;  // widest tile
+// Tensor memory (512 columns) with codes: beside the accumulators a ring of
+// unpacked weights, a step a slot.  Two accumulators leave four slots at 192
+// columns a tile; at 224 they would leave two, which is too few (4096 x 2560 x 2560,
+// k 7680: 159 us for 146).  Wider tiles have a single accumulator, whose
+// epilogue holds up the next tile's products: they are for grids of one tile a
+// pair (700 x 2560 x 9728, k 5120: 50 us, with 192 columns and so two rounds 76).
+constexpr int kSlotCols = kKStep / 4;
+__host__ __device__ constexpr int accumulators(int NT) { return NT > 192 ? 1 : 2; }
+__host__ __device__ constexpr int slots_of(int NT) {
+  return 512 - accumulators(NT) * NT >= 8 * kSlotCols ? 8 : 4;
+}
 constexpr int kUnpackWarp0 = 4, kUnpackGroups = 2, kEpiWarps = 8;
 // The stages that fit.  With codes they are a multiple of the unpacking groups,
 // so that a stage comes to the same group each time round: a group that met
@@ -83,7 +94,14 @@ constexpr int epi_warp0(bool codes) { return kUnpackWarp0 + (codes ? 4 * kUnpack
 constexpr int mma_threads(bool codes) { return 32 * (epi_warp0(codes) + kEpiWarps); }
 constexpr int kMmaSmem = kRingBytes + 1024;
 static_assert(2 * kMmaSmem > 228 * 1024, "one CTA per SM: it takes all of tensor memory");
-static_assert(stages_of(256, true) >= kUnpackGroups && stages_of(256, false) >= 2, "a ring");
+constexpr bool rings_hold() {
+  for (int NT = 32; NT <= kAccCols; NT += 32)
+    if (accumulators(NT) * NT + slots_of(NT) * kSlotCols > 512 || stages_of(NT, false) < 2 ||
+        slots_of(NT) % kUnpackGroups != 0 || stages_of(NT, true) < slots_of(NT))
+      return false;
+  return true;
+}
+static_assert(rings_hold(), "every width has its rings");
 
 struct Bars {
   uint64_t full[kMaxStages], empty[kMaxStages], codes[kMaxStages], accf[2], accfree[2], drain;
@@ -101,6 +119,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
   __shared__ int abort_flag;
   __shared__ __align__(16) float col_a[2][kAccCols], col_b[2][kAccCols];
   constexpr int kEpiWarp0 = epi_warp0(CODES);
+  constexpr int kTokens = CODES ? 0 : kOperand;  // offset of a stage's activations
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
@@ -109,6 +128,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
   const int ksteps = (a.K + kKStep - 1) / kKStep;
   const int tiles = MT * TT;
   const int stage_bytes = stage_bytes_of(NT, CODES);
+  const int nacc = CODES ? accumulators(NT) : 2, acc_cols = CODES ? NT : kAccCols;
+  const int slots = slots_of(NT);  // (of codes; from column `slot0` on)
+  const int slot0 = nacc * acc_cols;
   volatile int* ab = &abort_flag;
 
   if (wid == 2) {
@@ -154,7 +176,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     }
   };
   auto tokens = [&](int s, int k, int tt) {
-    tma_3d(smem_u32(ring + s * stage_bytes) + kOperand, &xmap, k * kKStep,
+    tma_3d(smem_u32(ring + s * stage_bytes) + kTokens, &xmap, k * kKStep,
            EPI == kOutFactors ? tt * per : tt * per + rank * half,
            EPI == kOutFactors ? rank : 0, in_leader(smem_u32(&bars.full[s])));
   };
@@ -210,12 +232,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     if (rank == 0) {  // ---- MMA issuer (the whole warp) ----
       const uint32_t idesc = instr_desc(256, NT), base = smem_u32(ring);
       const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
-      int s = 0, phase = 0, seg = 0;
+      int s = 0, phase = 0, seg = 0, slot = 0;
       bool ok = true, ready = false;
       for (int tile = pair; tile < tiles && ok; tile += npairs, ++seg) {
-        const int q = seg & 1;
-        if (seg >= 2 && !warp_wait(false, smem_u32(&bars.accfree[q]), ((seg >> 1) - 1) & 1, ab,
-                                   a.budget))
+        const int q = seg & (nacc - 1), use = nacc == 2 ? seg >> 1 : seg;
+        if (seg >= nacc &&
+            !warp_wait(false, smem_u32(&bars.accfree[q]), (use - 1) & 1, ab, a.budget))
           break;
         fence_after();
         for (int k = 0; k < ksteps; ++k) {
@@ -226,8 +248,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
           const uint32_t at = base + s * stage_bytes, done = smem_u32(&bars.empty[s]);
           if (++s == stages) s = 0, phase ^= 1;
           ready = bar_peek(smem_u32(&bars.full[s]), phase);  // (the next step's)
-          mma_step<true>(acc + q * kAccCols, operand_desc(at), operand_desc(at + kOperand), idesc,
-                         k > 0, done);
+          if (CODES) {
+            fence_after();
+            mma_step_tmem(acc + q * acc_cols, acc + slot0 + slot * kSlotCols, operand_desc(at),
+                          idesc, k > 0, done);
+            slot = (slot + 1) & (slots - 1);
+          } else {
+            mma_step<true>(acc + q * acc_cols, operand_desc(at), operand_desc(at + kOperand),
+                           idesc, k > 0, done);
+          }
         }
         if (ok) mma_commit<true>(smem_u32(&bars.accf[q]));
       }
@@ -238,16 +267,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     bar_wait(smem_u32(&bars.drain), 0u, &never, kDefaultWaitBudget);
   } else if (CODES && wid >= kUnpackWarp0 && wid < kEpiWarp0) {
     // ---- codes: a row a thread, the groups of four warps on alternate steps ----
-    // (a stage's codes land after its last MMAs are done: the operand is free)
     const int row = (wid & 3) * 32 + lane;
     const int mine = pair < tiles ? (tiles - pair + npairs - 1) / npairs * ksteps : 0;
-    int s = (wid - kUnpackWarp0) >> 2, phase = 0;
+    const uint32_t mem = tmem + slot0 + ((uint32_t)((wid & 3) * 32) << 16);
+    // stages of the step and of the one that had its slot before
+    int s = (wid - kUnpackWarp0) >> 2, phase = 0, before = s, before_phase = 0;
     for (int i = s; i < mine; i += kUnpackGroups) {
-      const bool got = bar_wait(smem_u32(&bars.codes[s]), phase, ab, a.budget);
+      bool got = bar_wait(smem_u32(&bars.codes[s]), phase, ab, a.budget);
+      if (got && i >= slots) {
+        got = bar_wait(smem_u32(&bars.empty[before]), before_phase, ab, a.budget);
+        if ((before += kUnpackGroups) >= stages) before -= stages, before_phase ^= 1;
+      }
       if (!__all_sync(0xffffffffu, got)) break;
-      unsigned char* stage = ring + s * stage_bytes;
-      unpack_row(stage + stage_bytes - kCodeBytes, stage, row);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      fence_after();
+      unpack_tmem(ring + s * stage_bytes + stage_bytes - kCodeBytes,
+                  mem + (uint32_t)(i & (slots - 1)) * kSlotCols, row);
+      fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive_cluster(in_leader(smem_u32(&bars.full[s])));
       if ((s += kUnpackGroups) >= stages) s -= stages, phase ^= 1;
@@ -259,14 +294,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     pdl_wait();
     int seg = 0;
     for (int tile = pair; tile < tiles; tile += npairs, ++seg) {
-      const int q = seg & 1;
+      const int q = seg & (nacc - 1), use = nacc == 2 ? seg >> 1 : seg, c = seg & 1;
       const int mt = tile % MT, tt = tile / MT;
       const int i = mt * 256 + rank * kHalfRows + quad * 32 + lane;
       const int t0 = tt * per;
       // the columns' scales (their buffer's last readers passed the barrier of
       // the tile between)
       bool odd = false;
-      if (et < per) odd = column_scales<EPI>(a, t0 + et, col_a[q][et], col_b[q][et]);
+      if (et < per) odd = column_scales<EPI>(a, t0 + et, col_a[c][et], col_b[c][et]);
       const float ws = EPI != kOutFactors && i < a.M ? a.wscale[i] : 0.f;
       const float bias = EPI == kOutDense && a.bias && i < a.M ? a.bias[i] : 0.f;
       // (with the columns' scales in place, whether any of them is not safe)
@@ -274,18 +309,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
         odd = bar_any(odd);
       else
         asm volatile("bar.sync 1, 256;" ::: "memory");
-      bool got = bar_wait(smem_u32(&bars.accf[q]), (seg >> 1) & 1, ab, a.budget);
+      bool got = bar_wait(smem_u32(&bars.accf[q]), use & 1, ab, a.budget);
       if (!__all_sync(0xffffffffu, got)) got = false;
       const bool all_ok = __all_sync(0xffffffffu, got);
       fence_after();
-      const uint32_t acc = tmem + q * kAccCols + ((uint32_t)(quad * 32) << 16);
+      const uint32_t acc = tmem + q * acc_cols + ((uint32_t)(quad * 32) << 16);
       if (all_ok) {
         for (int c0 = ch * 16; c0 < per; c0 += 32) {
           int v[16], lo[16];
           acc_load(acc + c0, v);
           if (EPI == kOutFactors) acc_load(acc + half + c0, lo);
           acc_wait();
-          finish<EPI>(a, v, lo, col_a[q] + c0, col_b[q] + c0, odd, ws, bias, i, t0 + c0, lane);
+          finish<EPI>(a, v, lo, col_a[c] + c0, col_b[c] + c0, odd, ws, bias, i, t0 + c0, lane);
         }
       }
       fence_before();
@@ -323,9 +358,10 @@ PairPlan pair_plan(const GemmArgs& a, Epilogue epi, int nsm) {
   PairPlan p = {};
   p.MT = (a.M + 255) / 256;
   long long best = -1;
-  for (int nt = 256; nt >= 32; nt -= 32) {
+  for (int nt = kAccCols; nt >= 32; nt -= 32) {
     const long long tt = ((long long)a.rows * (epi == kOutFactors ? 2 : 1) + nt - 1) / nt;
     const long long rounds = (p.MT * tt + pairs - 1) / pairs;
+    if (epi != kOutDense && accumulators(nt) == 1 && rounds > 1) continue;
     const long long cost = rounds * (nt + 32);
     if (best < 0 || cost < best) {
       best = cost;

@@ -172,6 +172,25 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uin
 #undef EXTERND_MMA_STEP
 }
 // the commit alone
+// The same on the pair's tile with the weights in tensor memory (`a`: 32 columns
+// of a step, 8 of an instruction's 32 bytes of K; both CTAs' at one address).
+__device__ __forceinline__ void mma_step_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                              bool accum, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b32 a;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n"
+      " setp.eq.b32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::2.kind::i8 [%0], [%1], %2, %3, p;\n"
+      " add.u32 a, %1, 8;\n add.u64 b, %2, 2;\n"
+      " @q tcgen05.mma.cta_group::2.kind::i8 [%0], [a], b, %3, t;\n"
+      " add.u32 a, %1, 16;\n add.u64 b, %2, 4;\n"
+      " @q tcgen05.mma.cta_group::2.kind::i8 [%0], [a], b, %3, t;\n"
+      " add.u32 a, %1, 24;\n add.u64 b, %2, 6;\n"
+      " @q tcgen05.mma.cta_group::2.kind::i8 [%0], [a], b, %3, t;\n"
+      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+      ".b64 [%5], %6;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accum), "r"(bar), "h"((uint16_t)3)
+      : "memory");
+}
 template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   if (PAIR)
@@ -382,6 +401,29 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const int (&v)[N], con
     else
       store_column((float*)a.y + at, a.ldy, left, y);
   }
+}
+
+// Unpacks a row's codes of one K step into its 32 columns of tensor memory
+// (`at`: the warp's lanes).  The halves of a row are read as in unpack_row.
+__device__ __forceinline__ void unpack_tmem(const unsigned char* codes, uint32_t at, int row) {
+  const uint4* src = (const uint4*)(codes + row * kCodeRow);
+  const int first = (row >> 2) & 1;
+  const uint4 x = src[first], y = src[first ^ 1];
+  const uint4 c[2] = {first ? y : x, first ? x : y};
+  uint32_t r[32];
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) r[4 * u + s] = (((const uint32_t*)c)[u] << (2 * s)) & kCodeMask;
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
+      " %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n"
+      " tcgen05.wait::st.sync.aligned;\n" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
 }
 
 // Unpacks a row's codes of one K step into its 128 (swizzled) operand bytes.
