@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       if (EPI != kOutPlanes) s = a.xscale[t0 + j * S + rank];
       if (EPI != kOutDense) z = a.z[t0 + j * S + rank];
     }
-    got = bar_wait(smem_u32(&bars.sums), 0u, ab, a.budget);
+    got = bar_wait<true>(smem_u32(&bars.sums), 0u, ab, a.budget);
     got = __all_sync(0xffffffffu, got);
     __syncwarp();
     cluster_arrive_relaxed();
