@@ -12,27 +12,26 @@
 // codes serve both.
 //
 // The K loop runs in steps of 128 bytes through a ring of six and more
-// shared-memory stages (128-byte swizzled rows).  Activations and 8-bit weights arrive by
-// TMA, which fills zeros past K, the last row and the last token.  Two-bit
-// codes arrive by TMA too (4 KB a step; five stages with codes of four steps
-// each were slower) and two groups of four warps unpack them, a row a thread,
-// two instructions for four codes, into the signed bytes +-64 the tensor core
-// reads.  Accumulators double up in tensor memory, so the epilogue of a tile
-// runs beside the K loop of the next one.
+// shared-memory stages (128-byte swizzled rows).  Activations and 8-bit weights
+// arrive by TMA, which fills zeros past K, the last row and the last token.
+// Two-bit codes arrive by TMA too (4 KB a step; five stages with codes of four
+// steps each were slower), and two groups of four warps unpack them, a row a
+// thread, two instructions for four codes, into the signed bytes +-64 of the
+// weight operand, which they store to tensor memory: through shared memory, the
+// unpacked codes going in and coming out were half of a saturated pipe's traffic
+// (factors of 1000 x 2560 x 2560, k 7680: 55.2 us, this way 50.4).  Where tensor
+// memory allows, accumulators double up, so the epilogue of a tile runs beside
+// the K loop of the next one.
 //
 // Bounds.  8-bit operands: the tensor cores; 8192 x 9728 x 2560 takes 125 us
 // alone (3.27 P operations a second, against 3.33 P for twice the measured
 // 16-bit rate), and 168 us run without a pause, where the power limit holds the
-// clock (2.43 P, against 2.79 P).  Codes: the shared-memory pipe beside them; a
-// step of a 256-column tile moves the unpacked codes in and both operands out,
-// about 576 cycles of that pipe for 512 of products.  Narrow tiles: a step takes
-// about 350 cycles however few its columns are (2560 x 9728 at 16 to 512 tokens:
-// 17.2 .. 17.7 us).  More stages, codes in contiguous blocks, a third producer and
-// codes read ahead of the fence all left that as it is, which points at the
-// matrix instructions, each reading its whole weight operand.
-// 4096 x 2560 x 2560, k 7680: 72 us the component sums, whose epilogue rounds 31
-// million of them, 94 us the second half with its two planes, 148 us in all, the
-// second half's start overlapping the first's end.
+// clock (2.43 P, against 2.79 P).  Few tiles (2560 x 9728 at 16 to 512 tokens:
+// 17.2 .. 17.7 us): a CTA's copies, 18 KB a step at some 50 bytes a cycle.  Codes,
+// 4096 x 2560 x 2560, k 7680: 70 us the component sums, whose epilogue rounds 31
+// million of them, 97 us the second half with its two planes (its products alone
+// take 82 % of that), 146 us in all, the second half's start overlapping the
+// first's end.
 //
 // Warp roles (per CTA): 0 TMA producer, 1 MMA issuer (even CTA of the pair),
 // 2 tensor-memory allocation, 3 TMA producer of the activations (8-bit weights

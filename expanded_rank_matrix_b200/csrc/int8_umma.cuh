@@ -66,11 +66,10 @@ __device__ __forceinline__ void bar_arrive(uint32_t a) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(a) : "memory");
 }
 // On the barrier of the pair's even CTA.  The scope is the default, the CTA:
-// what the arrival announces lies in the arriving CTA's own shared memory (or
-// is a tensor-memory read that is done), made visible to the tensor core by the
-// proxy fence before it.  (At cluster scope each arrival waited for all that
-// its warp had in flight: the factors of 4096 x 2560 x 2560, k 7680, took 418 us
-// for 186.)
+// what the arrival announces are tensor-memory stores and reads of the arriving
+// CTA, which have been waited for and which the fences of tcgen05 order before
+// the products.  (At cluster scope each arrival waited for all that its warp had
+// in flight: the factors of 4096 x 2560 x 2560, k 7680, took 418 us for 186.)
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t a) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
 }
