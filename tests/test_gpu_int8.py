@@ -388,6 +388,19 @@ def test_apply_long_prompts(t):
     R.check(y, *R.factors(*R.rows(x), B, C, D))
 
 
+@pytest.mark.parametrize("t", [17, 40, 70, 100, 130, 170, 200, 230, 256, 257, 300, 420, 512, 700,
+                               900, 1300, 1700])
+@pytest.mark.parametrize("mnk", [(2560, 300, 2600), (6000, 1300, 515), (300, 2049, 9000)])
+def test_apply_tile_widths(t, mnk):
+    """Tiles of every width, one and several of them a pair of CTAs, over few and
+    many steps."""
+    m, n, k = mnk
+    f, B, C, D = _factors(m, n, k, t)
+    x = _x(t, n, torch.bfloat16, t + 1)
+    y = X.apply_i8(X.pack_codes(f), x, out_dtype=torch.float32)
+    R.check(y, *R.factors(*R.rows(x), B, C, D))
+
+
 @pytest.mark.parametrize("t", [33, 48, 64, 80, 100, 128, 160, 250])
 def test_apply_split_over_long_dimensions(t):
     """Many steps of codes through rings of every depth (a ring's depth follows
