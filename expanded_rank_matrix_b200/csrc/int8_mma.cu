@@ -406,12 +406,12 @@ int launch(const GemmArgs& a, cudaStream_t st) {
 // Estimated time in units of 10 ns, fitted over the shapes of split_plan's (8-bit
 // operands, 2560 x 2560: 5.5 us at 16 tokens, 6.4 at 256, 7.7 at 700; 2560 x 9728:
 // 17.5, 17.2, 18.7).  The split kernel is taken where its estimate is below this:
-// over 2 .. 700 tokens of seven shapes the one taken was the slower one in four of
-// 98 cases, by at most 15 %.
+// over 2 .. 700 tokens of seven shapes the one taken was the slower one in five of
+// 98 cases, by at most 11 %; over five factored shapes in one of 60, by 5 %.
 long long mma_cost(const GemmArgs& a, Epilogue epi, int nsm) {
   const PairPlan p = pair_plan(a, epi, nsm);
-  const int step = epi == kOutDense ? 14 + p.NT * 6 / 100 : 19 + p.NT * 4 / 100;
-  return (epi == kOutDense ? 385 : 430) + p.rounds * ((a.K + kKStep - 1) / kKStep) * step;
+  const int step = (epi == kOutDense ? 14 : 17) + p.NT * 6 / 100;
+  return (epi == kOutDense ? 385 : 200) + p.rounds * ((a.K + kKStep - 1) / kKStep) * step;
 }
 
 int mma_gemm(const GemmArgs& a, Epilogue epi, cudaStream_t st) {
