@@ -306,8 +306,8 @@ int externd_quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, in
  *
  *   X       [rows][ldx] of xtype.  EXTERND_F32 / _F16 / _BF16: quantised within the call as
  *           externd_quantize_rows does (scratch: rows * (n + 19) bytes at most, for at
- *           most 65536 rows at a time; none for one row), rows that are not
- *           finite as there; xscale is ignored.  EXTERND_I8:
+ *           most 65536 rows at a time; none for one row up to n = 32768),
+ *           rows that are not finite as there; xscale is ignored.  EXTERND_I8:
  *           q itself, 16-byte aligned, ldx a multiple of 16 (every row, the
  *           last one too, holds ldx readable bytes; those past n do not
  *           count), with xscale [rows].

@@ -322,10 +322,11 @@ def test_apply_extreme_factors(t):
         fac = X.Factors(R.planes(b), R.planes(c), d, None, m, n)
         y = X.apply_i8(X.pack_codes(fac), xi)
         R.check(y, *R.factors(*R.rows(xi), b, c, d))
-    d = D.clone()
-    d[3] = float("nan")
-    y = X.apply_i8(X.pack_codes(X.Factors(R.planes(B), R.planes(C), d, None, m, n)), x)
-    assert torch.isnan(y).all()
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        d = D.clone()
+        d[3] = bad
+        y = X.apply_i8(X.pack_codes(X.Factors(R.planes(B), R.planes(C), d, None, m, n)), x)
+        assert torch.isnan(y).all()
     assert X.sync_status() == X.OK
 
 
