@@ -152,7 +152,9 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 // next one start (pdl_trigger) only after its own wait: when the call's later
 // kernels start, everything in front of the call has ended, so they may read
 // the call's weights, which none of its own kernels write, before their wait
-// (GemmArgs::early).
+// (GemmArgs::early).  Nothing that another kernel writes is read as read-only
+// data (__ldg, restrict pointers): the kernel in front may be writing it while
+// this one already runs, and such loads need not stay behind the wait.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -123,17 +123,16 @@ __global__ void __maxnreg__((row_regs<T>(VEC, WARP))) rows_kernel(const RowArgs<
   if (a.z) {
     squares = group_reduce<WARP, false>(squares, red[1]);
     if (tid == 0)
-      a.z[row] = (float)((double)__ldg(a.rho) * sqrt((double)squares) / kFullScale);
+      a.z[row] = (float)((double)a.rho[0] * sqrt((double)squares) / kFullScale);
   }
 }
 
 // z of rows that are already quantised: a CTA a row (long rows) or a warp a
 // row, four 16-byte loads of a thread in flight together.
 template <bool WARP>
-__global__ void __launch_bounds__(256) row_norm_kernel(const int8_t* __restrict__ q, int64_t ldq,
+__global__ void __launch_bounds__(256) row_norm_kernel(const int8_t* q, int64_t ldq,
                                                        int64_t rows, int n,
-                                                       const float* __restrict__ rho,
-                                                       float* __restrict__ z) {
+                                                       const float* rho, float* z) {
   __shared__ uint32_t red[32];
   pdl_wait();
   pdl_trigger();
@@ -149,7 +148,7 @@ __global__ void __launch_bounds__(256) row_norm_kernel(const int8_t* __restrict_
       const int j = j0 + u * G * 16;
       v[u] = make_int4(0, 0, 0, 0);
       if (j + 16 <= n)
-        v[u] = __ldg((const int4*)(x + j));
+        v[u] = *(const int4*)(x + j);
       else
         for (int e = j; e < n; ++e) sum += (int)x[e] * (int)x[e];
     }
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(256) row_norm_kernel(const int8_t* __restrict_
     }
   }
   const uint32_t total = group_reduce<WARP, false>((uint32_t)sum, red);
-  if (tid == 0) z[row] = (float)((double)__ldg(rho) * sqrt((double)total) / kFullScale);
+  if (tid == 0) z[row] = (float)((double)rho[0] * sqrt((double)total) / kFullScale);
 }
 
 template <typename T, int H, bool WARP>

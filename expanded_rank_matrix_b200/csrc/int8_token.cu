@@ -127,12 +127,12 @@ struct Weights<true> {
 constexpr int kEntries = 16, kSpan = 32 * kEntries;
 
 __device__ __forceinline__ void load_weights(uint4& w, const char* p) {
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                : "l"(p));
 }
 __device__ __forceinline__ void load_weights(uint32_t& w, const char* p) {
-  asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];" : "=r"(w) : "l"(p));
 }
 __device__ __forceinline__ uint32_t four(const uint4& w, int e) { return ((const uint32_t*)&w)[e]; }
 __device__ __forceinline__ uint32_t four(const uint32_t& w, int e) { return (w << (2 * e)) & kCodeMask; }
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
     scale = quantize_token<RAW, VEC>((const RAW*)a.raw, v, a.K, (a.K + 15) / 16 * 16, xs, rowred,
                                      &squares, EPI == kOutPlanes);
     if (EPI == kOutPlanes)
-      z = (float)((double)__ldg(a.rho) * sqrt((double)squares) / kFullScale);
+      z = (float)((double)a.rho[0] * sqrt((double)squares) / kFullScale);
     if (blockIdx.x == 0 && tid == 0) {
       if (EPI == kOutPlanes) a.scale_out[0] = scale, a.z_out[0] = z;
       if (isnan(scale)) atomicCAS(a.status, 0, EXTERND_ERR_NONFINITE);
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
     const int chunks = (a.K + 15) / 16;
     for (int e = tid; e < P * chunks; e += kTkThreads) {
       const int p = e >= chunks ? 1 : 0, j = (e - p * chunks) * 16;
-      uint4 v = __ldg((const uint4*)(a.x + p * a.plane + j));
+      uint4 v = *(const uint4*)(a.x + p * a.plane + j);
       if (a.K - j < 16) v = first_bytes(v, a.K - j);
       *(uint4*)(xs + 16 * e) = v;
     }
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
         x[u][p] = make_uint4(0u, 0u, 0u, 0u);
         if (kk < a.K)
           x[u][p] = SHARED ? *(const uint4*)(xs + p * ((a.K + 15) / 16 * 16) + kk)
-                           : __ldg((const uint4*)(a.x + p * a.plane + kk));
+                           : *(const uint4*)(a.x + p * a.plane + kk);
       }
     }
     if (!SHARED && k + U * kSpan > a.K) {  // the row may be padded with anything past K
