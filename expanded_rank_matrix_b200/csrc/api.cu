@@ -173,9 +173,11 @@ int externd_quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, in
   return externd::i8::quantize(X, type, ldx, rows, n, Q, ldq, scale, (cudaStream_t)stream);
 }
 
-int externd_matmul_i8(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W,
-                      int64_t ldw, const float* wscale, const float* bias, int64_t rows, int64_t n,
-                      int64_t m, void* Y, int ytype, int64_t ldy, externd_stream_t stream) {
+int externd_matmul_i8_ex(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W,
+                         int64_t ldw, const float* wscale, const float* bias, int64_t rows, int64_t n,
+                         int64_t m, void* Y, int ytype, int64_t ldy, int64_t wait_budget,
+                         externd_stream_t stream) {
+  if (wait_budget < 0) return EXTERND_ERR_INVALID_ARG;
   if (!rows_ok(rows) || !inner_ok(n) || !out_ok(m) || !float_type(ytype) ||
       (xtype != EXTERND_I8 && !float_type(xtype)))
     return EXTERND_ERR_INVALID_ARG;
@@ -185,7 +187,14 @@ int externd_matmul_i8(const void* X, int xtype, int64_t ldx, const float* xscale
   if (!activations_ok(X, xtype, ldx, xscale, n) || !float_matrix_ok(Y, ytype, ldy, m))
     return EXTERND_ERR_INVALID_ARG;
   return externd::i8::matmul(X, xtype, ldx, xscale, W, ldw, wscale, bias, rows, n, m, Y, ytype, ldy,
-                             (cudaStream_t)stream);
+                             wait_budget, (cudaStream_t)stream);
+}
+
+int externd_matmul_i8(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W,
+                      int64_t ldw, const float* wscale, const float* bias, int64_t rows, int64_t n,
+                      int64_t m, void* Y, int ytype, int64_t ldy, externd_stream_t stream) {
+  return externd_matmul_i8_ex(X, xtype, ldx, xscale, W, ldw, wscale, bias, rows, n, m, Y, ytype, ldy,
+                              0, stream);
 }
 
 int64_t externd_code_words(int64_t length) {
@@ -204,11 +213,12 @@ int externd_pack_codes(const uint32_t* packed_B, const uint32_t* packed_C, const
                                  (cudaStream_t)stream);
 }
 
-int externd_ternary_apply_i8(const uint32_t* codes_B, const uint32_t* codes_C, const float* D,
-                             const float* bound, int64_t m, int64_t n, int64_t k, const void* X,
-                             int xtype, int64_t ldx, const float* xscale, int64_t rows, void* Y,
-                             int ytype, int64_t ldy, externd_stream_t stream) {
-  if (!codes_B || !codes_C || !D || !bound) return EXTERND_ERR_INVALID_ARG;
+int externd_ternary_apply_i8_ex(const uint32_t* codes_B, const uint32_t* codes_C, const float* D,
+                                const float* bound, int64_t m, int64_t n, int64_t k, const void* X,
+                                int xtype, int64_t ldx, const float* xscale, int64_t rows, void* Y,
+                                int ytype, int64_t ldy, int64_t wait_budget,
+                                externd_stream_t stream) {
+  if (wait_budget < 0 || !codes_B || !codes_C || !D || !bound) return EXTERND_ERR_INVALID_ARG;
   if (!aligned16(codes_B) || !aligned16(codes_C) || !aligned4(D) || !aligned4(bound))
     return EXTERND_ERR_INVALID_ARG;
   if (!rows_ok(rows) || !out_ok(m) || !inner_ok(n) || !inner_ok(k) || !float_type(ytype) ||
@@ -218,7 +228,15 @@ int externd_ternary_apply_i8(const uint32_t* codes_B, const uint32_t* codes_C, c
   if (!activations_ok(X, xtype, ldx, xscale, n) || !float_matrix_ok(Y, ytype, ldy, m))
     return EXTERND_ERR_INVALID_ARG;
   return externd::i8::factors(codes_B, codes_C, D, bound, m, n, k, X, xtype, ldx, xscale, rows, Y,
-                              ytype, ldy, (cudaStream_t)stream);
+                              ytype, ldy, wait_budget, (cudaStream_t)stream);
+}
+
+int externd_ternary_apply_i8(const uint32_t* codes_B, const uint32_t* codes_C, const float* D,
+                             const float* bound, int64_t m, int64_t n, int64_t k, const void* X,
+                             int xtype, int64_t ldx, const float* xscale, int64_t rows, void* Y,
+                             int ytype, int64_t ldy, externd_stream_t stream) {
+  return externd_ternary_apply_i8_ex(codes_B, codes_C, D, bound, m, n, k, X, xtype, ldx, xscale, rows,
+                                     Y, ytype, ldy, 0, stream);
 }
 
 int externd_release_cache(void) {

@@ -88,13 +88,13 @@ int quantize(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8
 
 int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W, int64_t ldw,
            const float* wscale, const float* bias, int64_t rows, int64_t n, int64_t m, void* Y,
-           int ytype, int64_t ldy, cudaStream_t st) {
+           int ytype, int64_t ldy, long long budget, cudaStream_t st) {
   GemmArgs a = {};
   a.w = W; a.ldw = ldw; a.wscale = wscale; a.bias = bias;
   a.ytype = ytype; a.ldy = ldy;
   a.M = (int)m; a.K = (int)n;
   a.status = status_word();
-  a.budget = kDefaultWaitBudget;
+  a.budget = budget > 0 ? budget : kDefaultWaitBudget;
   if (!a.status) return EXTERND_ERR_CUDA;
   if (rows == 1 && xtype != EXTERND_I8 && n <= kTokenInner) {
     a.rows = 1;
@@ -132,7 +132,8 @@ int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int
 
 int factors(const uint32_t* codes_B, const uint32_t* codes_C, const float* D, const float* rho,
             int64_t m, int64_t n, int64_t k, const void* X, int xtype, int64_t ldx,
-            const float* xscale, int64_t rows, void* Y, int ytype, int64_t ldy, cudaStream_t st) {
+            const float* xscale, int64_t rows, void* Y, int ytype, int64_t ldy, long long budget,
+            cudaStream_t st) {
   int* status = status_word();
   if (!status) return EXTERND_ERR_CUDA;
   const int64_t chunk = std::min(rows, kPassRows);
@@ -150,7 +151,7 @@ int factors(const uint32_t* codes_B, const uint32_t* codes_C, const float* D, co
     const int64_t rr = std::min(chunk, rows - r0);
     GemmArgs a = {};
     a.status = status;
-    a.budget = kDefaultWaitBudget;
+    a.budget = budget > 0 ? budget : kDefaultWaitBudget;
     a.rows = (int)rr;
     const bool token = rows == 1 && xtype != EXTERND_I8 && n <= kTokenInner;
     if (token) {

@@ -56,10 +56,11 @@ int quantize(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8
              float* scale, cudaStream_t st);
 int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W, int64_t ldw,
            const float* wscale, const float* bias, int64_t rows, int64_t n, int64_t m, void* Y,
-           int ytype, int64_t ldy, cudaStream_t st);
+           int ytype, int64_t ldy, long long budget, cudaStream_t st);
 int factors(const uint32_t* codes_B, const uint32_t* codes_C, const float* D, const float* rho,
             int64_t m, int64_t n, int64_t k, const void* X, int xtype, int64_t ldx,
-            const float* xscale, int64_t rows, void* Y, int ytype, int64_t ldy, cudaStream_t st);
+            const float* xscale, int64_t rows, void* Y, int ytype, int64_t ldy, long long budget,
+            cudaStream_t st);
 
 }  // namespace i8
 }  // namespace externd

@@ -41,8 +41,8 @@
 // codes (each CTA: a stage's packed codes have landed),
 // empty (each CTA: the stage's MMAs are done), accf / accfree (an accumulator
 // is complete / read out).  Every wait is bounded; one that runs out raises
-// EXTERND_ERR_TIMEOUT, and the pair winds down without further waits than
-// those for its own copies and MMAs.
+// EXTERND_ERR_TIMEOUT, every role ends at its next wait, and the pair leaves
+// when its MMAs are done and its copies have landed (wind_down).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -106,6 +106,51 @@ struct Bars {
   uint64_t full[kMaxStages], empty[kMaxStages], codes[kMaxStages], accf[2], accfree[2], drain;
 };
 
+// What a pair tells itself about a launch that gives up: ring fills whose
+// weights and whose tokens this CTA and the other one have requested, and each
+// unpacking warp's next step.
+struct Wind {
+  int issued[2], other[2], other_gave_up, unpacked[4 * kUnpackGroups];
+};
+
+// The end of a pair of which a CTA has given up, all roles of both having
+// ended: no CTA leaves while copies are on their way to it.  The even CTA's
+// `full` barriers count the copies of both, and one of them may have stopped
+// before the other: up to the last fill that either has begun, each adds what
+// is missing of its own part (the bytes of copies that it did not request, the
+// arrivals of codes that it did not unpack), so each barrier completes with the
+// last copy that was requested.  A fill is at most a ring ahead of any part of
+// it (its stage is only free after the fill before it was complete), so no
+// barrier gets parts of two fills.
+template <bool CODES>
+__device__ __noinline__ void wind_down(Bars& bars, Wind& w, int stages, uint32_t half_bytes) {
+  const int tid = threadIdx.x, rank = (int)cluster_rank();
+  if (tid == 0)
+    for (int p = 0; p < 2; ++p) store_peer(in_peer(smem_u32(&w.other[p]), rank ^ 1), w.issued[p]);
+  __syncwarp();
+  cluster_sync();
+  const int fills = max(max(w.issued[0], w.issued[1]), max(w.other[0], w.other[1]));
+  const uint32_t weight_bytes = CODES ? 0u : (uint32_t)kOperand;
+  if (tid == 0) {
+    for (int f = w.issued[0]; f < fills; ++f) {
+      if (rank == 0) bar_expect(smem_u32(&bars.full[f % stages]), 2u * (weight_bytes + half_bytes));
+      if (!CODES) bar_complete(in_leader(smem_u32(&bars.full[f % stages])), weight_bytes);
+    }
+    for (int f = w.issued[1]; f < fills; ++f)
+      bar_complete(in_leader(smem_u32(&bars.full[f % stages])), half_bytes);
+  }
+  if (CODES && tid < 4 * kUnpackGroups)
+    for (int f = w.unpacked[tid]; f < fills; f += kUnpackGroups)
+      bar_arrive_cluster(in_leader(smem_u32(&bars.full[f % stages])));
+  __syncwarp();
+  if (tid == 0) {
+    if (CODES) wait_landed(bars.codes, w.issued[0], stages);
+    if (rank == 0) wait_landed(bars.full, fills, stages);
+  }
+  __syncwarp();
+  cluster_sync();
+}
+
 // MT tiles of 256 weight rows, TT tiles of NT tokens (kOutFactors: NT / 2).
 template <bool CODES, Epilogue EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 1)
@@ -116,6 +161,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
   __shared__ __align__(8) Bars bars;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
+  __shared__ Wind wind;
   __shared__ __align__(16) float col_a[2][kAccCols], col_b[2][kAccCols];
   constexpr int kEpiWarp0 = epi_warp0(CODES);
   constexpr int kTokens = CODES ? 0 : kOperand;  // offset of a stage's activations
@@ -152,6 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     bar_init(smem_u32(&bars.drain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     abort_flag = 0;
+    wind.other_gave_up = 0;
   }
   fence_before();
   __syncthreads();
@@ -192,7 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
         pdl_wait();
         for (int k = 0; k < ahead; ++k) tokens(k, k, pair / MT);
       }
-      int s = ahead == stages ? 0 : ahead, phase = ahead == stages ? 0 : 1;
+      int s = ahead == stages ? 0 : ahead, phase = ahead == stages ? 0 : 1, fills = ahead;
       bool ok = true;
       for (int tile = pair; tile < tiles && ok; tile += npairs) {
         const int wrow = (tile % MT) * 256 + rank * kHalfRows, tt = tile / MT;
@@ -203,9 +250,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
           }
           weights(s, k, wrow);
           if (CODES) tokens(s, k, tt);
+          ++fills;
           if (++s == stages) s = 0, phase ^= 1;
         }
       }
+      wind.issued[0] = fills;
+      if (CODES) wind.issued[1] = fills;
     }
   } else if (!CODES && wid == 3) {
     // 8-bit weights and the activations have a producer each: one for both was
@@ -213,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     // (333 x 1371 x 2001 product: 9.3 us for 8.8).
     if (elect_one()) {
       pdl_wait();
-      int s = 0, phase = 1;
+      int s = 0, phase = 1, fills = 0;
       bool ok = true;
       for (int tile = pair; tile < tiles && ok; tile += npairs) {
         const int tt = tile / MT;
@@ -223,9 +273,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
             break;
           }
           tokens(s, k, tt);
+          ++fills;
           if (++s == stages) s = 0, phase ^= 1;
         }
       }
+      wind.issued[1] = fills;
     }
   } else if (wid == 1) {
     if (rank == 0) {  // ---- MMA issuer (the whole warp) ----
@@ -261,9 +313,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
       }
       mma_commit<true>(smem_u32(&bars.drain));
     }
-    // both CTAs stay until every MMA is done and its arrivals have come
-    int never = 0;
-    bar_wait(smem_u32(&bars.drain), 0u, &never, kDefaultWaitBudget);
   } else if (CODES && wid >= kUnpackWarp0 && wid < kEpiWarp0) {
     // ---- codes: a row a thread, the groups of four warps on alternate steps ----
     const int row = (wid & 3) * 32 + lane;
@@ -271,7 +320,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     const uint32_t mem = tmem + slot0 + ((uint32_t)((wid & 3) * 32) << 16);
     // stages of the step and of the one that had its slot before
     int s = (wid - kUnpackWarp0) >> 2, phase = 0, before = s, before_phase = 0;
-    for (int i = s; i < mine; i += kUnpackGroups) {
+    int i = s;
+    for (; i < mine; i += kUnpackGroups) {
       bool got = bar_wait(smem_u32(&bars.codes[s]), phase, ab, a.budget);
       if (got && i >= slots) {
         got = bar_wait(smem_u32(&bars.empty[before]), before_phase, ab, a.budget);
@@ -286,6 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
       if (lane == 0) bar_arrive_cluster(in_leader(smem_u32(&bars.full[s])));
       if ((s += kUnpackGroups) >= stages) s -= stages, phase ^= 1;
     }
+    if (lane == 0) wind.unpacked[wid - kUnpackWarp0] = i;
   } else if (wid >= kEpiWarp0) {
     // ---- epilogue: warp w reads lanes 32 (w % 4) .., one half of the columns ----
     const int quad = wid & 3, ch = (wid - kEpiWarp0) >> 2;
@@ -327,15 +378,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
       if (lane == 0) bar_arrive_cluster(in_leader(smem_u32(&bars.accfree[q])));
     }
   }
-  // (after a timeout: the pair's copies in flight land within the delay)
-  if (*ab) {
-    const long long t0 = clock64();
-    while (clock64() - t0 < 2000000LL) {
-    }
-  }
   fence_before();
   __syncthreads();
+  // Both CTAs stay until every MMA is done and its arrivals have come.  (The
+  // wait starts behind the CTA's other roles: it is bounded, and a launch may
+  // take longer than that from its start.)
+  if (wid == 1) {
+    int never = 0;
+    bar_wait(smem_u32(&bars.drain), 0u, &never, kDefaultWaitBudget);
+  }
+  if (tid == 0 && abort_flag) store_peer(in_peer(smem_u32(&wind.other_gave_up), rank ^ 1), 1);
+  __syncwarp();
   cluster_sync();
+  if (abort_flag || wind.other_gave_up)
+    wind_down<CODES>(bars, wind, stages, (uint32_t)(half * kKStep));
   if (wid == 2) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)

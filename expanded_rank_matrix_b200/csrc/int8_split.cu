@@ -23,7 +23,9 @@
 //
 // Warp roles: 0 TMA producer, 1 MMA issuer, 2 tensor-memory allocation, 4..11
 // unpack codes (two groups of four, alternate steps), then read the
-// accumulator out and finish.  Waits are bounded as in int8_mma.cu.
+// accumulator out and finish.  Waits are bounded as in int8_mma.cu; a CTA that
+// has given up leaves when its MMAs are done, the copies that it requested have
+// landed and every CTA's sums have come or have been counted as not coming.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -87,11 +89,6 @@ __device__ __forceinline__ void tma_3d_own(uint32_t dst, const void* map, int x,
       "{%2, %3, %4}], [%5];" ::"r"(dst),
       "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
-}
-__device__ __forceinline__ uint32_t in_peer(uint32_t addr, int rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
 }
 // adds to a word of a CTA's shared memory; 4 bytes count on its barrier
 __device__ __forceinline__ void remote_add(uint32_t at, int v, uint32_t bar) {
@@ -181,7 +178,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   int* sums = (int*)(ring + stages * stage_bytes_of(NT, CODES));
   __shared__ __align__(8) SplitBars bars;
   __shared__ uint32_t tmem_base;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, issued;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int rank = (int)cluster_rank();
   const int i0 = (int)(blockIdx.x / S) * 128, per = NT / P, t0 = blockIdx.y * per;
@@ -250,6 +247,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   }
   if (a.early) pdl_trigger();
 
+  int unpacked = steps;
   if (wid == 0) {
     if (producer) {  // ---- TMA producer ----
       auto tokens = [&](int i) {
@@ -266,12 +264,14 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       else
         pdl_trigger();
       for (int i = 0; i < ahead; ++i) tokens(i);
-      for (int i = ahead; i < steps; ++i) {
+      int i = ahead;
+      for (; i < steps; ++i) {
         const int s = i % stages;
         if (!bar_wait(smem_u32(&bars.empty[s]), ((i / stages) + 1) & 1, ab, a.budget)) break;
         weights(i);
         tokens(i);
       }
+      issued = i;
     }
   } else if (wid == 1) {
     // ---- MMA issuer (the whole warp) ----
@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     if (CODES) {  // ---- codes: a row a thread, the two groups on alternate steps ----
       const int row = quad * 32 + lane;
       // (a stage's codes land after its last MMAs are done: the operand is free)
-      for (int i = half; i < steps; i += kUnpackGroups) {
+      int i = half;
+      for (; i < steps; i += kUnpackGroups) {
         const int s = i % stages;
         const bool got = bar_wait(smem_u32(&bars.codes[s]), (i / stages) & 1, ab, a.budget);
         if (!__all_sync(0xffffffffu, got)) break;
@@ -305,16 +306,17 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         __syncwarp();
         if (lane == 0) bar_arrive(smem_u32(&bars.full[s]));
       }
+      unpacked = i;
     }
     // ---- the CTA's sums to the tokens' owners ----
     bool got = bar_wait(smem_u32(&bars.accf), 0u, ab, a.budget);
     got = __all_sync(0xffffffffu, got);
     __syncwarp();
     cluster_wait();
+    const uint32_t bar = smem_u32(&bars.sums);
     if (got) {
       fence_after();
       const uint32_t at = smem_u32(sums) + (uint32_t)(quad * 32 + lane) * 4u;
-      const uint32_t bar = smem_u32(&bars.sums);
       for (int c = half * 16; c < NT; c += 32) {
         int v[16];
         acc_load(tmem + ((uint32_t)(quad * 32) << 16) + c, v);
@@ -333,7 +335,16 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
           }
         }
       }
+    } else if (lane == 0) {
+      // no sums: the owners must not wait for them, nor leave before those of
+      // the other CTAs have come
+      for (int c = half * 16; c < NT; c += 32)
+        for (int e = 0; e < 16; ++e) {
+          const int u = P == 2 && c + e >= per ? c + e - per : c + e;
+          if (u < left) bar_complete(in_peer(bar, u % S), 128u);
+        }
     }
+    __syncwarp();
     // ---- the CTA's own tokens: a warp each, a lane four neighbouring rows ----
     pdl_wait();
     const int r = 4 * lane, i = i0 + r;
@@ -366,12 +377,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       }
     }
   }
-  // (after a timeout: copies in flight land within the delay)
-  if (*ab) {
-    const long long w0 = clock64();
-    while (clock64() - w0 < 2000000LL) {
-    }
-  }
   __syncwarp();
   if (wid < kFinishWarp0) {
     cluster_wait();
@@ -379,6 +384,19 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   }
   fence_before();
   __syncthreads();
+  if (abort_flag) {
+    // a fill's barrier also counts the warps that unpack it
+    if (CODES && wid >= kFinishWarp0 && lane == 0)
+      for (int f = unpacked; f < issued; f += kUnpackGroups) bar_arrive(smem_u32(&bars.full[f % stages]));
+    __syncwarp();
+    if (tid == 0) {
+      int never = 0;
+      if (CODES) wait_landed(bars.codes, issued, stages);
+      wait_landed(bars.full, issued, stages);
+      bar_wait<true>(smem_u32(&bars.sums), 0u, &never, kDefaultWaitBudget);
+    }
+    __syncwarp();
+  }
   cluster_wait();  // (no CTA leaves while another may still add to its sums)
   if (wid == 2) {
     fence_after();

@@ -41,6 +41,15 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
 }
+// the same shared-memory address in the CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t in_peer(uint32_t addr, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void store_peer(uint32_t at, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -72,6 +81,13 @@ __device__ __forceinline__ void bar_arrive(uint32_t a) {
 // in flight: the factors of 4096 x 2560 x 2560, k 7680, took 418 us for 186.)
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t a) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+}
+// In the place of copies (or remote additions) that were not made: `bytes` of
+// what a barrier of the cluster expects count as arrived.
+__device__ __forceinline__ void bar_complete(uint32_t a, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(a),
+               "r"(bytes)
+               : "memory");
 }
 // CLUSTER: the data that the barrier announces came from other CTAs (the split
 // kernel's sums).  All others announce the CTA's own shared memory, or tensor
@@ -107,21 +123,31 @@ __device__ __forceinline__ bool bar_peek(uint32_t a, uint32_t parity) {
       : "memory");
   return ok != 0u;
 }
-// Bounded wait; gives up early once the CTA has recorded a timeout.
+// Bounded wait; gives up early once the CTA has recorded a timeout.  (The clock
+// is read between the tests: a test may pause for longer than a short budget.)
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t a, uint32_t parity, volatile int* abort,
                                          long long budget) {
-  if (bar_test<CLUSTER>(a, parity)) return true;
+  if (CLUSTER ? bar_test<true>(a, parity) : bar_peek(a, parity)) return true;
   const long long t0 = clock64();
   unsigned spins = 0;
-  while (!bar_test<CLUSTER>(a, parity)) {
+  do {
     if (((++spins) & 15u) == 0u && *abort) return false;
     if (clock64() - t0 > budget) {
       *abort = 1;
       return false;
     }
-  }
+  } while (!bar_test<CLUSTER>(a, parity));
   return true;
+}
+// The end of a kernel that has given up: the CTA keeps its shared memory until
+// the last `stages` of `fills` ring fills have landed (a stage's earlier fills
+// have, or the stage would not have been filled again).  Bounded, by the
+// default whatever the launch's budget is.
+__device__ __forceinline__ void wait_landed(const uint64_t* bars, int fills, int stages) {
+  int never = 0;
+  for (int f = max(0, fills - stages); f < fills; ++f)
+    bar_wait(smem_u32(&bars[f % stages]), (uint32_t)(f / stages) & 1u, &never, kDefaultWaitBudget);
 }
 // The same for a whole warp that has tested the barrier before (`ready`), so
 // that the test's latency passes behind other work.

@@ -37,7 +37,8 @@ EXPORTS = ("externd_rank", "externd_decompose", "externd_decompose_ex", "externd
            "externd_decompose_block_traced", "externd_rank_for_energy",
            "externd_ternary_apply", "externd_probe_read_bandwidth", "externd_release_cache",
            "externd_quantize_rows", "externd_matmul_i8", "externd_code_words",
-           "externd_pack_codes", "externd_ternary_apply_i8")
+           "externd_pack_codes", "externd_ternary_apply_i8", "externd_matmul_i8_ex",
+           "externd_ternary_apply_i8_ex")
 
 _lib = None
 _calls = None  # the 8-bit calls' marshalling, bound to the library
@@ -91,6 +92,8 @@ def load(path: str = LIB_PATH):
     L.externd_matmul_i8.argtypes = [_vp, ctypes.c_int, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64,
                                     _i64, _vp, ctypes.c_int, _i64, _vp]
     L.externd_matmul_i8.restype = ctypes.c_int
+    L.externd_matmul_i8_ex.argtypes = L.externd_matmul_i8.argtypes[:-1] + [_i64, _vp]
+    L.externd_matmul_i8_ex.restype = ctypes.c_int
     L.externd_code_words.argtypes = [_i64]
     L.externd_code_words.restype = _i64
     L.externd_pack_codes.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp]
@@ -98,6 +101,8 @@ def load(path: str = LIB_PATH):
     L.externd_ternary_apply_i8.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, ctypes.c_int,
                                            _i64, _vp, _i64, _vp, ctypes.c_int, _i64, _vp]
     L.externd_ternary_apply_i8.restype = ctypes.c_int
+    L.externd_ternary_apply_i8_ex.argtypes = L.externd_ternary_apply_i8.argtypes[:-1] + [_i64, _vp]
+    L.externd_ternary_apply_i8_ex.restype = ctypes.c_int
     L.externd_probe_read_bandwidth.argtypes = [ctypes.c_int, _vp, _i64, ctypes.c_int,
                                                ctypes.POINTER(ctypes.c_int64), _vp]
     L.externd_probe_read_bandwidth.restype = ctypes.c_int

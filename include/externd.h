@@ -327,6 +327,18 @@ int externd_matmul_i8(const void* X, int xtype, int64_t ldx, const float* xscale
                       int64_t m, void* Y, int ytype, int64_t ldy, externd_stream_t stream);
 
 /*
+ * externd_matmul_i8_ex -- externd_matmul_i8 with
+ *   wait_budget  upper bound, in SM clock cycles, on each wait of the tensor-core
+ *           kernels (0: the default of about one second).  A wait that runs out
+ *           raises EXTERND_ERR_TIMEOUT; Y is then undefined, and the kernel
+ *           leaves once its copies and matrix products have ended.
+ */
+int externd_matmul_i8_ex(const void* X, int xtype, int64_t ldx, const float* xscale, const int8_t* W,
+                         int64_t ldw, const float* wscale, const float* bias, int64_t rows, int64_t n,
+                         int64_t m, void* Y, int ytype, int64_t ldy, int64_t wait_budget,
+                         externd_stream_t stream);
+
+/*
  * externd_code_words -- 32-bit words of one row of `length` packed ternary
  * codes (two bits an entry, rows padded to 128 entries); 0 when length is out
  * of 1 .. EXTERND_I8_MAX_OUT.
@@ -375,6 +387,16 @@ int externd_ternary_apply_i8(const uint32_t* codes_B, const uint32_t* codes_C, c
                              const float* bound, int64_t m, int64_t n, int64_t k, const void* X,
                              int xtype, int64_t ldx, const float* xscale, int64_t rows, void* Y,
                              int ytype, int64_t ldy, externd_stream_t stream);
+
+/*
+ * externd_ternary_apply_i8_ex -- externd_ternary_apply_i8 with the wait budget of
+ * externd_matmul_i8_ex.
+ */
+int externd_ternary_apply_i8_ex(const uint32_t* codes_B, const uint32_t* codes_C, const float* D,
+                                const float* bound, int64_t m, int64_t n, int64_t k, const void* X,
+                                int xtype, int64_t ldx, const float* xscale, int64_t rows, void* Y,
+                                int ytype, int64_t ldy, int64_t wait_budget,
+                                externd_stream_t stream);
 
 /*
  * externd_decompose_noalloc -- externd_decompose (block == 1 only) without

@@ -83,3 +83,12 @@ def test_code_words():
     assert X.code_words(1) == 8 and X.code_words(128) == 8 and X.code_words(129) == 16
     assert X.code_words(2560) == 160
     assert X.code_words(0) == 0 and X.code_words(X.I8_MAX_OUT + 1) == 0
+
+
+def test_wait_budget_must_not_be_negative(lib):
+    mm = [P, X.I8, 64, P, P, 64, P, None, 0, 64, 8, P, X.F32, 8]
+    assert lib.externd_matmul_i8_ex(*mm, -1, None) == X.ERR_INVALID_ARG
+    assert lib.externd_matmul_i8_ex(*mm, 1, None) == X.OK
+    app = [P, P, P, P, 8, 64, 16, P, X.F32, 64, None, 0, P, X.F32, 8]
+    assert lib.externd_ternary_apply_i8_ex(*app, -1, None) == X.ERR_INVALID_ARG
+    assert lib.externd_ternary_apply_i8_ex(*app, 1, None) == X.OK
