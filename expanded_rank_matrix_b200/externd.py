@@ -460,7 +460,8 @@ class FactorCodes:
 
 def pack_codes(f: Factors, stream: Optional[torch.cuda.Stream] = None) -> FactorCodes:
     """Lays factors out once for apply_i8 (externd_pack_codes): those of a
-    decomposition, or its first components (truncate)."""
+    decomposition, or its first components (truncate).  The codes stand for the
+    factors as they are now."""
     device = _device_of(f.D, f.packed_B, f.packed_C)
     if stream is not None:
         with _elsewhere(device, stream):
@@ -469,7 +470,9 @@ def pack_codes(f: Factors, stream: Optional[torch.cuda.Stream] = None) -> Factor
         with torch.cuda.device(device):
             return pack_codes(f)
     k = f.k
-    D, pB, pC = f.D.contiguous(), f.packed_B.contiguous(), f.packed_C.contiguous()
+    # (D is kept beside its bound: a copy, which a later change of f.D does not reach)
+    D = f.D.clone(memory_format=torch.contiguous_format)
+    pB, pC = f.packed_B.contiguous(), f.packed_C.contiguous()
     if pB.shape != (k, 2, words(f.m)) or pC.shape != (k, 2, words(f.n)):
         raise ValueError("packed factors and D do not belong together")
     if (pB.dtype, pC.dtype, D.dtype) != (torch.int32, torch.int32, torch.float32):

@@ -376,7 +376,8 @@ int externd_pack_codes(const uint32_t* packed_B, const uint32_t* packed_C, const
  * activations.  fp32 arithmetic, rounded once to ytype.  A NaN or an infinity in
  * D makes the bound one, and every result NaN.
  *
- *   codes_B, codes_C, bound: from externd_pack_codes; D [k] the same as there.
+ *   codes_B, codes_C, bound: from externd_pack_codes; D [k] with the values that it
+ *            had there (larger ones would leave h's 16 bits).
  *   X, xtype, ldx, xscale, rows, Y, ytype, ldy: as for externd_matmul_i8.
  * Scratch: for each of at most 4096 rows at a time n + 2 k + 54 bytes at
  * most, stream-ordered from the inference pool (externd_ternary_apply).
