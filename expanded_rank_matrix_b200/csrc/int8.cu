@@ -19,10 +19,19 @@ namespace {
 
 constexpr int64_t pad16(int64_t v) { return (v + 15) & ~(int64_t)15; }
 
-// Tokens that one pass of the factored product takes: its component sums (two
-// bytes for each token and component) then stay within tens of megabytes, of
-// the order of the L2 cache, however long the prompt is.
-constexpr int64_t kPassRows = 4096;
+// Tokens that one pass takes: at most so many, and no more than the scratch of
+// kScratchBytes holds, in whole tiles (the longest inner dimensions leave 512
+// tokens to the factored product, 1792 to the dense one).  The factored
+// product's component sums, two bytes for each token and component, stay of
+// the order of the L2 cache with 4096 tokens of a few thousand components.
+constexpr int64_t kPassRows = 4096, kDensePassRows = 65536;
+constexpr int64_t kScratchBytes = (int64_t)256 << 20, kTileRows = 256;
+
+int64_t pass_rows(int64_t rows, int64_t most, int64_t bytes_per_row) {
+  if (bytes_per_row > 0)
+    most = std::min(most, std::max(kScratchBytes / bytes_per_row / kTileRows * kTileRows, kTileRows));
+  return std::min(rows, most);
+}
 
 int64_t type_size(int type) { return type == EXTERND_F32 ? 4 : type == EXTERND_I8 ? 1 : 2; }
 
@@ -105,7 +114,7 @@ int matmul(const void* X, int xtype, int64_t ldx, const float* xscale, const int
   }
   Scratch ws(st);
   const int64_t ldq = pad16(n);
-  const int64_t chunk = std::min<int64_t>(rows, 65536);
+  const int64_t chunk = pass_rows(rows, kDensePassRows, xtype != EXTERND_I8 ? ldq + 4 : 0);
   int rc = EXTERND_OK;
   if (xtype != EXTERND_I8) rc = ws.take((size_t)(chunk * (ldq + 4)));
   for (int64_t r0 = 0; rc == EXTERND_OK && r0 < rows; r0 += chunk) {
@@ -136,8 +145,9 @@ int factors(const uint32_t* codes_B, const uint32_t* codes_C, const float* D, co
             cudaStream_t st) {
   int* status = status_word();
   if (!status) return EXTERND_ERR_CUDA;
-  const int64_t chunk = std::min(rows, kPassRows);
   const int64_t ldq = pad16(n), ldh = pad16(k);
+  const int64_t chunk =
+      pass_rows(rows, kPassRows, (xtype == EXTERND_I8 ? 0 : ldq) + 2 * ldh + 8);
   const int64_t qbytes = xtype == EXTERND_I8 ? 0 : chunk * ldq;
   const int64_t plane = chunk * ldh;
   Scratch ws(st);

@@ -305,8 +305,8 @@ int externd_quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, in
  * rounded once to ytype.
  *
  *   X       [rows][ldx] of xtype.  EXTERND_F32 / _F16 / _BF16: quantised within the call as
- *           externd_quantize_rows does (scratch: rows * (n + 19) bytes at most, for at
- *           most 65536 rows at a time; none for one row up to n = 32768),
+ *           externd_quantize_rows does (scratch: rows * (n + 19) bytes, 256 MiB
+ *           at most; none for one row up to n = 32768),
  *           rows that are not finite as there; xscale is ignored.  EXTERND_I8:
  *           q itself, 16-byte aligned, ldx a multiple of 16 (every row, the
  *           last one too, holds ldx readable bytes; those past n do not
@@ -379,8 +379,9 @@ int externd_pack_codes(const uint32_t* packed_B, const uint32_t* packed_C, const
  *   codes_B, codes_C, bound: from externd_pack_codes; D [k] with the values that it
  *            had there (larger ones would leave h's 16 bits).
  *   X, xtype, ldx, xscale, rows, Y, ytype, ldy: as for externd_matmul_i8.
- * Scratch: for each of at most 4096 rows at a time n + 2 k + 54 bytes at
- * most, stream-ordered from the inference pool (externd_ternary_apply).
+ * Scratch: n + 2 k + 54 bytes at most for each of at most 4096 rows at a time,
+ * 256 MiB at most, stream-ordered from the inference pool
+ * (externd_ternary_apply).
  * Returns EXTERND_OK, EXTERND_ERR_INVALID_ARG, EXTERND_ERR_OOM or
  * EXTERND_ERR_CUDA.
  */

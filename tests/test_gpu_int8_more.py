@@ -1,11 +1,11 @@
 """More of the 8-bit inference operators: what a change of the factors after their
-packing may not reach.  Needs a B200."""
+packing may not reach, and the memory that a call takes.  Needs a B200."""
 import pytest
 import torch
 
 from expanded_rank_matrix_b200 import externd as X
 from tests import int8_ref as R
-from tests.test_gpu_int8 import _factors, _x
+from tests.test_gpu_int8 import _factors, _held, _x
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +26,36 @@ def test_factors_changed_after_packing(t):
     f.packed_B.zero_()
     f.packed_C.zero_()
     assert torch.equal(X.apply_i8(c, x), want) and torch.equal(X.apply_i8(head, x), want_head)
+
+
+def _taken(call):
+    """The call's result, and the device memory that it leaves in the library's pool."""
+    call()  # (code and torch's own blocks)
+    torch.cuda.synchronize()
+    assert X.load().externd_release_cache() == X.OK
+    before = torch.cuda.mem_get_info()[0]
+    y = call()
+    torch.cuda.synchronize()
+    return y, before - torch.cuda.mem_get_info()[0]
+
+
+def test_scratch_of_the_longest_ranks():
+    """4096 tokens of the largest rank: passes of fewer tokens, and the same
+    results over their seams."""
+    t, m, n, k = 4096, 9, 40, X.I8_MAX_INNER
+    f, B, C, D = _factors(m, n, k, 1)
+    c, x = X.pack_codes(f), _x(t, n, torch.float32, 2)
+    y, taken = _taken(lambda: X.apply_i8(c, x))
+    assert taken <= 300 << 20
+    q, s = R.rows(x)
+    for i in (0, 510, 766, 1534, 2302, 4092):  # (passes of 768 tokens)
+        R.check(y[i:i + 4], *R.factors(q[i:i + 4], s[i:i + 4], B, C, D))
+
+
+def test_scratch_of_the_longest_rows():
+    t, m, n = 8192, 16, X.I8_MAX_INNER
+    x, w = _x(t, n, torch.float16, 1), _held(m, n, 2)
+    y, taken = _taken(lambda: X.matmul_i8(x, w, out_dtype=torch.float32))
+    assert taken <= 300 << 20
+    for i in (0, 1790, 1792, 3583, 8188):  # (passes of 1792)
+        R.check(y[i:i + 4], *R.dense(*R.rows(x[i:i + 4]), w.q, w.scale))
