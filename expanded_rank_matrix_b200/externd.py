@@ -54,7 +54,7 @@ class ExterndError(RuntimeError):
 
 def load(path: str = LIB_PATH):
     """Loads the library (no GPU needed) and declares the signatures."""
-    global _lib, _calls
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -110,13 +110,6 @@ def load(path: str = LIB_PATH):
     L.externd_sync_status.restype = ctypes.c_int
     L.externd_release_cache.argtypes = []
     L.externd_release_cache.restype = ctypes.c_int
-    try:
-        from . import _calls as native
-    except ImportError as e:
-        raise RuntimeError("_calls.so is not built; run __graft_entry__.build()") from e
-    native.bind(*(ctypes.cast(f, _vp).value for f in (
-        L.externd_quantize_rows, L.externd_matmul_i8, L.externd_ternary_apply_i8)))
-    _calls = native
     _lib = L
     return L
 
@@ -406,7 +399,19 @@ def quantize_rows(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -
 
 
 def _loaded():
-    load()
+    """The 8-bit calls' marshalling, bound to the library when the first of them
+    is made (nothing else needs it)."""
+    global _calls
+    L = load()
+    if _calls is None:
+        try:
+            from . import _calls as native
+        except ImportError as e:
+            raise RuntimeError(f"_calls.so cannot be loaded: {e} "
+                               "(__graft_entry__.build() builds it)") from e
+        native.bind(*(ctypes.cast(f, _vp).value for f in (
+            L.externd_quantize_rows, L.externd_matmul_i8, L.externd_ternary_apply_i8)))
+        _calls = native
     return _calls
 
 
