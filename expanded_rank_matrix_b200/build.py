@@ -12,6 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libexternd.so")
 CALLS = os.path.join(HERE, "_calls.so")  # the native part of the Python binding
+CALLS_STAMP = os.path.join(HERE, "_build", "_calls.interfaces")  # what it was built against
 # (-static-global-template-stub=false: the sequential kernel template is
 # instantiated in its own units and launched from seq_als.cu)
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
@@ -22,7 +23,16 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _interfaces() -> str:
+    """The torch and the Python whose interfaces _calls.so is bound to."""
+    import importlib.metadata
+    import sysconfig
+    return f"torch {importlib.metadata.version('torch')} {sysconfig.get_config_var('SOABI')}"
+
+
 def _stale_calls() -> bool:
+    if not os.path.exists(CALLS_STAMP) or open(CALLS_STAMP).read() != _interfaces():
+        return True
     deps = (os.path.join(CSRC, "calls.cpp"), os.path.join(HERE, "..", "include", "externd.h"))
     return not os.path.exists(CALLS) or any(os.path.getmtime(d) > os.path.getmtime(CALLS)
                                             for d in deps)
@@ -47,6 +57,9 @@ def build_calls() -> str:
                     "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
                     "-ltorch_cuda", "-ltorch", "-ltorch_python"], check=True)
     os.replace(tmp, CALLS)
+    os.makedirs(os.path.dirname(CALLS_STAMP), exist_ok=True)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(_interfaces())
     return CALLS
 
 

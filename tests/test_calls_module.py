@@ -51,3 +51,12 @@ def test_module_is_bound_when_it_is_there():
         X.quantize_rows(torch.zeros(1, 4))
 
 
+def test_another_torch_makes_the_module_stale(monkeypatch):
+    """The module is bound to the C++ interface of one torch (and of one Python)."""
+    assert not B._stale_calls()
+    monkeypatch.setattr(B, "_interfaces", lambda: "another torch")
+    assert B._stale_calls()
+    monkeypatch.undo()
+    assert not B._stale_calls()
+    import torch
+    assert torch.__version__ in B._interfaces()
