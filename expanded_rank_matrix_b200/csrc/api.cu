@@ -42,6 +42,16 @@ bool inner_ok(int64_t n) { return n >= 1 && n <= EXTERND_I8_MAX_INNER; }
 bool out_ok(int64_t m) { return m >= 1 && m <= EXTERND_I8_MAX_OUT; }
 bool rows_ok(int64_t r) { return r >= 0 && r <= EXTERND_I8_MAX_ROWS; }
 
+// Returns and clears a status word.
+int take_status(int* p) {
+  int v = 0;
+  const int zero = 0;
+  if (!p || cudaMemcpy(&v, p, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
+      cudaMemcpy(p, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
+    return EXTERND_ERR_CUDA;
+  return v;
+}
+
 }  // namespace
 
 extern "C" {
@@ -245,16 +255,15 @@ int externd_release_cache(void) {
   return a != EXTERND_OK ? a : b;
 }
 
-int externd_sync_status(externd_stream_t stream) {
+int externd_sync_decompose_status(externd_stream_t stream) {
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return EXTERND_ERR_CUDA;
-  int* p = externd::status_word_ptr();
-  if (!p) return EXTERND_ERR_CUDA;
-  int v = 0;
-  if (cudaMemcpy(&v, p, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return EXTERND_ERR_CUDA;
-  const int zero = 0;
-  if (cudaMemcpy(p, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
-    return EXTERND_ERR_CUDA;
-  return v;
+  return take_status(externd::status_word_ptr());
+}
+
+int externd_sync_status(externd_stream_t stream) {
+  const int v = externd_sync_decompose_status(stream);
+  const int w = v == EXTERND_ERR_CUDA ? v : take_status(externd::i8::status_word());
+  return v != EXTERND_OK ? v : w;
 }
 
 }  // extern "C"

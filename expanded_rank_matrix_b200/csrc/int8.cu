@@ -17,6 +17,8 @@ namespace i8 {
 
 namespace {
 
+__device__ int g_status = 0;  // (first error wins)
+
 constexpr int64_t pad16(int64_t v) { return (v + 15) & ~(int64_t)15; }
 
 // Tokens that one pass takes: at most so many, and no more than the scratch of
@@ -46,19 +48,23 @@ int gemm(const GemmArgs& a, Epilogue epi, cudaStream_t st) {
   return mma_gemm(a, epi, st);
 }
 
-// The device's status word (its address does not change; looking it up costs
-// as much as a small launch's arguments).
+}  // namespace
+
+// (its address does not change; looking it up costs as much as a small launch's
+// arguments)
 int* status_word() {
   static std::atomic<int*> at[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
   int* p = at[dev].load(std::memory_order_relaxed);
   if (!p) {
-    p = status_word_ptr();
+    if (cudaGetSymbolAddress((void**)&p, g_status) != cudaSuccess) return nullptr;
     at[dev].store(p, std::memory_order_relaxed);
   }
   return p;
 }
+
+namespace {
 
 // Stream-ordered scratch from the library's pool, freed on the stream.
 struct Scratch {

@@ -9,6 +9,8 @@
 namespace externd {
 namespace i8 {
 
+// The current device's sticky status word of the 8-bit calls (null: a CUDA error).
+int* status_word();
 // Q, scale from X; with rho also z = fl(rho |q|_2 / 32512) of each row.
 int quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, int64_t n, int8_t* Q,
                   int64_t ldq, float* scale, const float* rho, float* z, int* status, cudaStream_t st);

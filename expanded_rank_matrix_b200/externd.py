@@ -38,7 +38,7 @@ EXPORTS = ("externd_rank", "externd_decompose", "externd_decompose_ex", "externd
            "externd_ternary_apply", "externd_probe_read_bandwidth", "externd_release_cache",
            "externd_quantize_rows", "externd_matmul_i8", "externd_code_words",
            "externd_pack_codes", "externd_ternary_apply_i8", "externd_matmul_i8_ex",
-           "externd_ternary_apply_i8_ex")
+           "externd_ternary_apply_i8_ex", "externd_sync_decompose_status")
 
 _lib = None
 _calls = None  # the 8-bit calls' marshalling, bound to the library
@@ -108,6 +108,8 @@ def load(path: str = LIB_PATH):
     L.externd_probe_read_bandwidth.restype = ctypes.c_int
     L.externd_sync_status.argtypes = [_vp]
     L.externd_sync_status.restype = ctypes.c_int
+    L.externd_sync_decompose_status.argtypes = [_vp]
+    L.externd_sync_decompose_status.restype = ctypes.c_int
     L.externd_release_cache.argtypes = []
     L.externd_release_cache.restype = ctypes.c_int
     _lib = L
@@ -196,7 +198,7 @@ def decompose(A: torch.Tensor, mu: float, tau: float, iters: int,
     out = alloc_factors(m, n, k, A.device)
     decompose_into(out, A, mu, tau, iters, w, block, stream, flags, sweeps)
     if check:
-        st = sync_status(stream)
+        st = _decompose_status(stream)
         if st != OK:
             raise ExterndError(st, "externd_decompose (device)")
     return out
@@ -253,7 +255,7 @@ def decompose_traced(A: torch.Tensor, mu: float, tau: float, iters: int,
         _stream(stream))
     if rc != OK:
         raise ExterndError(rc, "externd_decompose_traced")
-    status = sync_status(stream)
+    status = _decompose_status(stream)
     if check and status != OK:
         raise ExterndError(status, "externd_decompose_traced (device)")
     return out, Trace(comps, tb[:nt], tr[:nt], tf[:nt], stats, iters), status
@@ -533,6 +535,12 @@ def sync_status(stream: Optional[torch.cuda.Stream] = None) -> int:
     return int(load().externd_sync_status(_stream(stream)))
 
 
+def _decompose_status(stream: Optional[torch.cuda.Stream]) -> int:
+    """The status without that of the 8-bit calls, which is not a
+    decomposition's to report or to clear."""
+    return int(load().externd_sync_decompose_status(_stream(stream)))
+
+
 def release_cache() -> int:
     """externd_release_cache: drops the block path's cached graphs (with
     their workspaces) and trims the inference scratch pools; returns the C
@@ -603,7 +611,7 @@ def decompose_block_traced(A: torch.Tensor, mu: float, tau: float, iters: int, b
         _ptr(rows) if nt else None, wait_budget, _stream(stream))
     if rc != OK:
         raise ExterndError(rc, "externd_decompose_block_traced")
-    status = sync_status(stream)
+    status = _decompose_status(stream)
     if check and status != OK:
         raise ExterndError(status, "externd_decompose_block_traced (device)")
     tr = BlockTrace(blocks, uv[:nt], rows[:nt], iters, block)

@@ -42,7 +42,8 @@ extern "C" {
 #define EXTERND_ERR_OOM (-3)         /* scratch allocation failed               */
 #define EXTERND_ERR_NO_COOP (-4)     /* the persistent grid cannot be resident  */
 #define EXTERND_ERR_TIMEOUT (-5)     /* a bounded device-side wait ran out      */
-#define EXTERND_ERR_NONFINITE (-6)   /* NaN/Inf in A, or w not finite and > 0   */
+#define EXTERND_ERR_NONFINITE (-6)   /* NaN/Inf in A or in a row to quantise, or
+                                        w not finite and > 0                    */
 #define EXTERND_ERR_SCRATCH_LIMIT (-7) /* problem too large for the fixed scratch  */
 
 typedef struct CUstream_st* externd_stream_t; /* same object as cudaStream_t */
@@ -283,7 +284,7 @@ int externd_ternary_apply(const uint32_t* packed_B, const uint32_t* packed_C, co
  *         scale is 0; at most 127 in magnitude).
  * A row with an infinity or a NaN gets scale NaN and q = 0 (so products with
  * it are NaN, and no other row is touched) and raises EXTERND_ERR_NONFINITE
- * in the status word.
+ * in the 8-bit calls' status word (externd_sync_status).
  *
  *   X      [rows][ldx] of `type` (EXTERND_F32 / _F16 / _BF16), aligned to its
  *          element, ldx >= n elements between rows.
@@ -498,9 +499,18 @@ int externd_release_cache(void);
  * current device's status word: EXTERND_OK, or the first device-side error
  * (EXTERND_ERR_TIMEOUT, EXTERND_ERR_NONFINITE) raised by any call on this
  * device since the last read; EXTERND_ERR_CUDA if the synchronisation
- * itself failed.
+ * itself failed.  Errors of the 8-bit calls (whose rows that are not finite are
+ * data of a user's requests, and speak through their NaN results too) are held
+ * in a word of their own, which is read after the other one's.
  */
 int externd_sync_status(externd_stream_t stream);
+
+/*
+ * externd_sync_decompose_status -- externd_sync_status without the 8-bit calls:
+ * an error that they raised is neither returned nor cleared.  What a
+ * decomposition is checked with while such calls run beside it.
+ */
+int externd_sync_decompose_status(externd_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,5 +1,6 @@
 """More of the 8-bit inference operators: what a change of the factors after their
-packing may not reach, and the memory that a call takes.  Needs a B200."""
+packing may not reach, the memory that a call takes, and whose errors are
+whose.  Needs a B200."""
 import pytest
 import torch
 
@@ -59,3 +60,32 @@ def test_scratch_of_the_longest_rows():
     assert taken <= 300 << 20
     for i in (0, 1790, 1792, 3583, 8188):  # (passes of 1792)
         R.check(y[i:i + 4], *R.dense(*R.rows(x[i:i + 4]), w.q, w.scale))
+
+
+@pytest.mark.parametrize("block", [1, 32])
+def test_decompositions_beside_rows_that_are_not_finite(block):
+    """A row that is not finite is no error of a decomposition made after it, and
+    is still reported behind one."""
+    x = _x(3, 64, torch.float32, 1)
+    x[1, 5] = float("nan")
+    A = _x(96, 64, torch.float32, 2)
+    bad = A.clone()
+    bad[0, 0] = float("inf")
+    assert X.sync_status() == X.OK
+    f = X.decompose(A, 0.5, 0.5, 2, block=block)
+    for call in (lambda: X.quantize_rows(x), lambda: X.apply_i8(X.pack_codes(f), x),
+                 lambda: X.matmul_i8(x, X.Quantized(*_rows(A)))):
+        call()
+        g = X.decompose(A, 0.5, 0.5, 2, block=block)
+        assert torch.equal(g.D, f.D)
+        assert X.sync_status() == X.ERR_NONFINITE and X.sync_status() == X.OK
+        call()
+        with pytest.raises(X.ExterndError) as e:
+            X.decompose(bad, 0.5, 0.5, 2, block=block)
+        assert e.value.code == X.ERR_NONFINITE
+        assert X.sync_status() == X.ERR_NONFINITE and X.sync_status() == X.OK
+
+
+def _rows(A):
+    r = X.quantize_rows(A)
+    return r.q, r.scale
