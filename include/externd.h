@@ -371,11 +371,20 @@ int externd_pack_codes(const uint32_t* packed_B, const uint32_t* packed_C, const
  *   y_ti = scale_t (z_t sum_c B_ic h_tc)    (whole-number sum, exact)
  * h has 16 bits and is held as two 8-bit planes, so both products are 8-bit
  * products with whole-number sums: results do not depend on how a call is
- * batched.  The fixed scale z_t costs log2(sqrt(n)) of h's bits against a
- * scale from the true maximum, and saves the pass over all sums that would
- * find it; what is left (a step of z_t) is below the step of the 8-bit
- * activations.  fp32 arithmetic, rounded once to ytype.  A NaN or an infinity in
+ * batched.  fp32 arithmetic, rounded once to ytype.  A NaN or an infinity in
  * D makes the bound one, and every result NaN.
+ *
+ * Accuracy.  z_t is known before the sums, which saves the pass over them that
+ * would find their maximum, but the bound lies about sqrt(n) above a usual sum,
+ * so most of h's 16 bits stay unused.  The rounding of the sums moves y_ti by
+ * scale_t z_t / 2 at most for each nonzero of B's row i, and by about
+ * scale_t z_t sqrt(nonzeros / 12) as a rule.  It grows with n and may exceed what
+ * the 8-bit activations cost.  Relative errors of y (activations' rounding;
+ * this one): factors of a decomposed 512 x 512 matrix 0.70 %, 0.14 %; of a
+ * decomposed 512 x 2560 one 0.80 %, 0.80 %; random factors whose D falls with
+ * the root of the component's number, n 2560 and k 7680, 0.84 %, 1.1 %, and
+ * n 9728, k 5120, 0.94 %, 1.5 %.  (A scale from the largest sum of each token
+ * would leave less than 0.03 % in each of these.)
  *
  *   codes_B, codes_C, bound: from externd_pack_codes; D [k] with the values that it
  *            had there (larger ones would leave h's 16 bits).
