@@ -388,7 +388,8 @@ class Quantized:
 def quantize_rows(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> Quantized:
     """Symmetric 8-bit quantisation of the rows of X [..., n] (fp32, fp16 or
     bf16) with one scale a row (externd_quantize_rows): tokens of activations,
-    output channels of a weight matrix."""
+    output channels of a weight matrix.  Not differentiable: no gradient, of
+    either mode, reaches X or comes from it."""
     if stream is not None:
         with _elsewhere(X.get_device(), stream):
             return quantize_rows(X)
@@ -423,7 +424,8 @@ def matmul_i8(X, W: Quantized, bias: Optional[torch.Tensor] = None, out_dtype=No
     each token and each output channel (externd_matmul_i8).  X: [..., n] fp32,
     fp16 or bf16, quantised within the call, or Quantized rows (shared by
     several products).  The output is [..., m] of out_dtype (default: X's
-    type; fp32 for Quantized).  Not differentiable: no gradient reaches X."""
+    type; fp32 for Quantized).  Not differentiable: no gradient, of either mode,
+    reaches X, W or the bias or comes from them."""
     if stream is not None:
         with _elsewhere(W.q.get_device(), stream):
             return matmul_i8(X, W, bias, out_dtype)
@@ -498,7 +500,9 @@ def pack_codes(f: Factors, stream: Optional[torch.cuda.Stream] = None) -> Factor
 def apply_i8(c: FactorCodes, X, out_dtype=None,
              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """X (B diag(D) C)^T on 8-bit activations, from the packed codes
-    (externd_ternary_apply_i8).  X and out_dtype as for matmul_i8."""
+    (externd_ternary_apply_i8, which says what the rounding of the component
+    sums costs).  X and out_dtype as for matmul_i8.  Not differentiable: no
+    gradient, of either mode, reaches X or the factors or comes from them."""
     if stream is not None:
         with _elsewhere(c.D.get_device(), stream):
             return apply_i8(c, X, out_dtype)

@@ -1,6 +1,6 @@
 """More of the 8-bit inference operators: what a change of the factors after their
 packing may not reach, the memory that a call takes, and whose errors are
-whose.  Needs a B200."""
+whose, the smallest numbers of each type, and gradients.  Needs a B200."""
 import pytest
 import torch
 
@@ -89,3 +89,46 @@ def test_decompositions_beside_rows_that_are_not_finite(block):
 def _rows(A):
     r = X.quantize_rows(A)
     return r.q, r.scale
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n", [24, 2560, 2561])
+def test_subnormal_rows(dtype, n):
+    """Rows whose largest magnitude is a subnormal of the type, down to its
+    smallest, and rows that mix subnormals with normal numbers."""
+    tiny = torch.finfo(dtype).tiny
+    step = {torch.float32: 2.0 ** -149, torch.float16: 2.0 ** -24, torch.bfloat16: 2.0 ** -133}[dtype]
+    g = torch.Generator().manual_seed(n)
+    rows = [torch.full((n,), step, dtype=torch.float64), torch.zeros(n, dtype=torch.float64)]
+    rows[1][n // 2] = -step
+    for top in (2, 3, 126, 127, 128, tiny / step - 1, tiny / step, 300 * tiny / step):
+        v = torch.randint(-int(top), int(top) + 1, (n,), generator=g).double() * step
+        v[n - 1] = top * step
+        rows.append(v)
+    x = torch.stack(rows).to(dtype)
+    assert (x.double().abs().amax(1) > 0).all()
+    x = x.cuda()
+    r = X.quantize_rows(x)
+    q, s = R.rows(x)
+    assert torch.equal(r.scale.double(), s) and torch.equal(r.q.double(), q)
+    w = _held(40, n, 2)
+    R.check(X.matmul_i8(x, w, out_dtype=torch.float32), *R.dense(q, s, w.q, w.scale))
+    for i in range(len(rows)):  # (a single row is quantised within the product)
+        R.check(X.matmul_i8(x[i:i + 1], w, out_dtype=torch.float32),
+                *R.dense(q[i:i + 1], s[i:i + 1], w.q, w.scale))
+    assert X.sync_status() == X.OK
+
+
+def test_no_gradients():
+    f, *_ = _factors(20, 32, 30, 1)
+    w, c = _held(20, 32, 2), X.pack_codes(f)
+    x = _x(3, 32, torch.float32, 3).requires_grad_()
+    b = torch.zeros(20, device="cuda", requires_grad=True)
+    r = X.quantize_rows(x)
+    for y in (r.q, r.scale, X.matmul_i8(x, w, bias=b), X.apply_i8(c, x)):
+        assert not y.requires_grad and y.grad_fn is None
+    # what does have a gradient keeps its own
+    (x.sum() + X.apply_i8(c, x).sum()).backward()
+    assert torch.equal(x.grad, torch.ones_like(x)) and b.grad is None
+    for make in (X.quantize_rows, X.matmul_i8, X.apply_i8):
+        assert "Not differentiable" in make.__doc__
