@@ -53,7 +53,8 @@ int64_t pad16(int64_t v) { return (v + 15) / 16 * 16; }
 int64_t row_bytes(const at::Tensor& q) { return q.size(0) > 1 ? q.stride(0) : pad16(q.size(1)); }
 
 // A tensor [..., n] as rows at one distance with their elements side by side:
-// itself, or a copy.
+// itself, or a copy.  (Views that stand for the negatives of what they hold are
+// copied too.)
 struct Rows {
   at::Tensor held;  // keeps a copy alive
   const void* at = nullptr;
@@ -63,13 +64,14 @@ Rows rows_of(const at::Tensor& X) {
   Rows r;
   if (X.dim() == 0 || X.size(-1) == 0) refuse("X must have at least one column");
   r.n = X.size(-1);
-  if (X.is_contiguous()) {
+  if (X.is_contiguous() && !X.is_neg()) {
     r.rows = X.numel() / r.n;
     r.ld = r.n;
     r.at = X.const_data_ptr();
     return r;
   }
   r.held = X.dim() == 2 ? X : X.reshape({-1, r.n});
+  if (r.held.is_neg()) r.held = r.held.resolve_neg();
   r.rows = r.held.size(0);
   if ((r.n > 1 && r.held.stride(1) != 1) || (r.rows > 1 && r.held.stride(0) < r.n))
     r.held = r.held.contiguous();
@@ -213,7 +215,7 @@ PyObject* matmul_i8(PyObject*, PyObject* const* args, Py_ssize_t n) {
         refuse("bias must be fp32 [" + std::to_string(m) + "]");
       if (!bias.is_cuda() || bias.get_device() != device)
         refuse("expected tensors on one CUDA device");
-      bias = bias.contiguous();
+      bias = bias.contiguous().resolve_neg();
     }
     at::Tensor Y = allocate(a.out, a.out_type, device);
     void* yp = Y.mutable_data_ptr();

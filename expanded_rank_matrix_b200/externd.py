@@ -351,7 +351,7 @@ def _elsewhere(index: int, stream: torch.cuda.Stream):
 def _vector(v: torch.Tensor, length: int, what: str) -> torch.Tensor:
     if v.dtype != torch.float32 or v.dim() != 1 or v.shape[0] != length:
         raise ValueError(f"{what} must be fp32 [{length}]")
-    return v if v.is_contiguous() else v.contiguous()
+    return v.contiguous().resolve_neg()
 
 
 @dataclass(frozen=True)

@@ -1,12 +1,12 @@
 """More of the 8-bit inference operators: what a change of the factors after their
 packing may not reach, the memory that a call takes, and whose errors are
-whose, the smallest numbers of each type, and gradients.  Needs a B200."""
+whose, the smallest numbers of each type, gradients, and negated views.  Needs a B200."""
 import pytest
 import torch
 
 from expanded_rank_matrix_b200 import externd as X
 from tests import int8_ref as R
-from tests.test_gpu_int8 import _factors, _held, _x
+from tests.test_gpu_int8 import _factors, _gen, _held, _x
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +132,24 @@ def test_no_gradients():
     assert torch.equal(x.grad, torch.ones_like(x)) and b.grad is None
     for make in (X.quantize_rows, X.matmul_i8, X.apply_i8):
         assert "Not differentiable" in make.__doc__
+
+
+def test_negated_views():
+    """Tensors that hold the negatives of their values (the imaginary part of a
+    conjugate), in the shapes that need no copy for their layout."""
+    z = torch.randn(5, 8, dtype=torch.complex64, generator=_gen(1), device="cuda").conj().imag
+    assert z.is_neg()
+    for x in (z, z[:, :1], z[:1, :1], torch._neg_view(_x(4, 32, torch.float32, 2))):
+        assert x.is_neg()
+        n = x.shape[1]
+        plain = x + 0.0
+        assert not plain.is_neg()
+        w, c = _held(6, n, 3), X.pack_codes(_factors(6, n, 9, 4)[0])
+        a, b = X.quantize_rows(x), X.quantize_rows(plain)
+        assert torch.equal(a.q, b.q) and torch.equal(a.scale, b.scale)
+        assert torch.equal(X.matmul_i8(x, w), X.matmul_i8(plain, w))
+        assert torch.equal(X.apply_i8(c, x), X.apply_i8(c, plain))
+    v = torch._neg_view(_x(1, 6, torch.float32, 5)[0])
+    x, w = _x(2, 16, torch.float32, 6), _held(6, 16, 7)
+    assert torch.equal(X.matmul_i8(x, w, bias=v), X.matmul_i8(x, w, bias=v + 0.0))
+    assert torch.equal(X.matmul_i8(x, X.Quantized(w.q, v)), X.matmul_i8(x, X.Quantized(w.q, v + 0.0)))
