@@ -160,5 +160,16 @@ __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// 16 bytes that another kernel may have written: a plain load that stays behind
+// pdl_wait, as volatile statements keep their order.  (Named global: through a
+// generic address 8192 x 9728 bf16 rows take 41.8 us to quantise, this way 40.3.)
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 }  // namespace i8
 }  // namespace externd

@@ -25,7 +25,7 @@ template <typename T, bool VEC>
 __device__ __forceinline__ void load_vec(const T* x, int j, int n, int G, T (&v)[16 / sizeof(T)]) {
   constexpr int E = 16 / sizeof(T);
   if (VEC && j + E <= n) {
-    *(uint4*)v = *(const uint4*)(x + j);
+    *(uint4*)v = load16(x + j);
   } else {
     const int step = VEC ? 1 : G;
 #pragma unroll

@@ -142,22 +142,22 @@ __global__ void __launch_bounds__(256) row_norm_kernel(const int8_t* q, int64_t 
   const int8_t* x = q + row * ldq;
   int sum = 0;
   for (int j0 = tid * 16; j0 < n; j0 += 4 * G * 16) {
-    int4 v[4];
+    uint4 v[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int j = j0 + u * G * 16;
-      v[u] = make_int4(0, 0, 0, 0);
+      v[u] = make_uint4(0u, 0u, 0u, 0u);
       if (j + 16 <= n)
-        v[u] = *(const int4*)(x + j);
+        v[u] = load16(x + j);
       else
         for (int e = j; e < n; ++e) sum += (int)x[e] * (int)x[e];
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      sum = __dp4a(v[u].x, v[u].x, sum);
-      sum = __dp4a(v[u].y, v[u].y, sum);
-      sum = __dp4a(v[u].z, v[u].z, sum);
-      sum = __dp4a(v[u].w, v[u].w, sum);
+      sum = __dp4a((int)v[u].x, (int)v[u].x, sum);
+      sum = __dp4a((int)v[u].y, (int)v[u].y, sum);
+      sum = __dp4a((int)v[u].z, (int)v[u].z, sum);
+      sum = __dp4a((int)v[u].w, (int)v[u].w, sum);
     }
   }
   const uint32_t total = group_reduce<WARP, false>((uint32_t)sum, red);

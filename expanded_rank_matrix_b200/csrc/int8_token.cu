@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
     const int chunks = (a.K + 15) / 16;
     for (int e = tid; e < P * chunks; e += kTkThreads) {
       const int p = e >= chunks ? 1 : 0, j = (e - p * chunks) * 16;
-      uint4 v = *(const uint4*)(a.x + p * a.plane + j);
+      uint4 v = load16(a.x + p * a.plane + j);
       if (a.K - j < 16) v = first_bytes(v, a.K - j);
       *(uint4*)(xs + 16 * e) = v;
     }
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kTkThreads) token_kernel(const GemmArgs a) {
         x[u][p] = make_uint4(0u, 0u, 0u, 0u);
         if (kk < a.K)
           x[u][p] = SHARED ? *(const uint4*)(xs + p * ((a.K + 15) / 16 * 16) + kk)
-                           : *(const uint4*)(a.x + p * a.plane + kk);
+                           : load16(a.x + p * a.plane + kk);
       }
     }
     if (!SHARED && k + U * kSpan > a.K) {  // the row may be padded with anything past K
