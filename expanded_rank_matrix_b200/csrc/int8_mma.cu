@@ -110,7 +110,7 @@ struct Bars {
 // weights and whose tokens this CTA and the other one have requested, and each
 // unpacking warp's next step.
 struct Wind {
-  int issued[2], other[2], other_gave_up, unpacked[4 * kUnpackGroups];
+  int issued[2], other[2], gave_up, unpacked[4 * kUnpackGroups];
 };
 
 // The end of a pair of which a CTA has given up, all roles of both having
@@ -198,7 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
     bar_init(smem_u32(&bars.drain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     abort_flag = 0;
-    wind.other_gave_up = 0;
+    wind.gave_up = 0;
   }
   fence_before();
   __syncthreads();
@@ -313,6 +313,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
       }
       mma_commit<true>(smem_u32(&bars.drain));
     }
+    // Both CTAs stay until every MMA is done and its arrivals have come.  (The odd
+    // CTA waits from the start on: the bound is one for each tile, and one.)
+    int never = 0;
+    bar_wait(smem_u32(&bars.drain), 0u, &never,
+             kDefaultWaitBudget * ((tiles - pair + npairs - 1) / npairs + 1));
   } else if (CODES && wid >= kUnpackWarp0 && wid < kEpiWarp0) {
     // ---- codes: a row a thread, the groups of four warps on alternate steps ----
     const int row = (wid & 3) * 32 + lane;
@@ -380,17 +385,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mma_threads(CODES), 
   }
   fence_before();
   __syncthreads();
-  // Both CTAs stay until every MMA is done and its arrivals have come.  (The
-  // wait starts behind the CTA's other roles: it is bounded, and a launch may
-  // take longer than that from its start.)
-  if (wid == 1) {
-    int never = 0;
-    bar_wait(smem_u32(&bars.drain), 0u, &never, kDefaultWaitBudget);
+  if (tid == 0 && abort_flag) {
+    wind.gave_up = 1;
+    store_peer(in_peer(smem_u32(&wind.gave_up), rank ^ 1), 1);
   }
-  if (tid == 0 && abort_flag) store_peer(in_peer(smem_u32(&wind.other_gave_up), rank ^ 1), 1);
   __syncwarp();
   cluster_sync();
-  if (abort_flag || wind.other_gave_up)
+  if (wind.gave_up)
     wind_down<CODES>(bars, wind, stages, (uint32_t)(half * kKStep));
   if (wid == 2) {
     fence_after();

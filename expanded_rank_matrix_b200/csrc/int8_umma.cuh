@@ -124,11 +124,11 @@ __device__ __forceinline__ bool bar_peek(uint32_t a, uint32_t parity) {
   return ok != 0u;
 }
 // Bounded wait; gives up early once the CTA has recorded a timeout.  (The clock
-// is read between the tests: a test may pause for longer than a short budget.)
+// is read between the tests, each of which may pause for some microseconds.)
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t a, uint32_t parity, volatile int* abort,
                                          long long budget) {
-  if (CLUSTER ? bar_test<true>(a, parity) : bar_peek(a, parity)) return true;
+  if (bar_test<CLUSTER>(a, parity)) return true;
   const long long t0 = clock64();
   unsigned spins = 0;
   do {

@@ -37,9 +37,11 @@ def _apply(c, x, budget):
     return y
 
 
-# few tiles, split over clusters; many, on pairs of CTAs; more than the GPU holds
-@pytest.mark.parametrize("t,m,n", [(32, 2560, 9728), (100, 300, 4096), (1024, 2560, 2560),
-                                   (3000, 5000, 1999)])
+# few tiles, split over clusters; many, on pairs of CTAs; more than the GPU holds.
+# (Inner dimensions long enough that an epilogue waits for its products longer
+# than a test of a barrier may pause.)
+@pytest.mark.parametrize("t,m,n", [(32, 2560, 40000), (100, 300, 65536), (1024, 2560, 20000),
+                                   (3000, 5000, 9999)])
 def test_product_waits_run_out(t, m, n):
     x, w = _held(t, n, 1), _held(m, n, 2)
     _matmul(x, w, 1)
@@ -50,9 +52,9 @@ def test_product_waits_run_out(t, m, n):
         R.check(y, *R.dense(x.q, x.scale, w.q, w.scale))
 
 
-@pytest.mark.parametrize("t,m,n,k", [(24, 512, 8192, 384), (100, 384, 512, 8192),
-                                     (16, 9728, 2560, 5120), (1024, 2560, 1300, 2570),
-                                     (3000, 2560, 700, 3333)])
+@pytest.mark.parametrize("t,m,n,k", [(24, 512, 65536, 384), (100, 384, 512, 65536),
+                                     (16, 9728, 2560, 30000), (1024, 2560, 1300, 20000),
+                                     (3000, 2560, 700, 20000)])
 def test_factors_waits_run_out(t, m, n, k):
     f, B, C, D = _factors(m, n, k, t)
     c, x = X.pack_codes(f), _x(t, n, torch.float32, 1)
@@ -64,7 +66,7 @@ def test_factors_waits_run_out(t, m, n, k):
         R.check(y, *R.factors(*R.rows(x), B, C, D))
 
 
-@pytest.mark.parametrize("budget", [1, 300, 1000, 2000, 4000, 8000])
+@pytest.mark.parametrize("budget", [1, 30, 300, 1000, 2000, 4000, 8000, 16000])
 def test_waits_run_out_anywhere(budget):
     """Budgets that run out at some wait or other, in some CTAs and not in
     others: nothing hangs, and calls that report no timeout are exact."""
