@@ -24,11 +24,6 @@ __host__ __device__ constexpr int64_t code_words(int64_t len) { return (len + 12
 constexpr uint32_t kCodeMask = 0xC0C0C0C0u;
 constexpr int kCodeShift = 6;
 
-// Largest inner dimension: the sums of n products of 8-bit values and
-// 64 * (ternary) stay below 2^31, and those of 8-bit values and codes below
-// 2^24 (exact in fp32).
-constexpr int64_t kMaxInner = EXTERND_I8_MAX_INNER;
-
 // The 16-bit component sums: |h| <= 127 * 256, so both 8-bit planes of
 // h = 256 hi + lo (lo in -128 .. 127) fit.
 constexpr double kFullScale = 32512.0;

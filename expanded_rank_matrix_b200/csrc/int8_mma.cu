@@ -23,15 +23,15 @@
 // memory allows, accumulators double up, so the epilogue of a tile runs beside
 // the K loop of the next one.
 //
-// Bounds.  8-bit operands: the tensor cores; 8192 x 9728 x 2560 takes 125 us
-// alone (3.27 P operations a second, against 3.33 P for twice the measured
-// 16-bit rate), and 168 us run without a pause, where the power limit holds the
-// clock (2.43 P, against 2.79 P).  Few tiles (2560 x 9728 at 16 to 512 tokens:
-// 17.2 .. 17.7 us): a CTA's copies, 18 KB a step at some 50 bytes a cycle.  Codes,
-// 4096 x 2560 x 2560, k 7680: 70 us the component sums, whose epilogue rounds 31
-// million of them, 97 us the second half with its two planes (its products alone
-// take 82 % of that), 146 us in all, the second half's start overlapping the
-// first's end.
+// Bounds.  8-bit operands: the tensor cores, active in 85 % of the cycles, and
+// the clock that the power limit leaves; 8192 x 9728 x 2560 takes 124 us alone
+// (3.30 P operations a second; twice the measured 16-bit rate is 3.33 P), 138 a
+// few in a row, and 168 us run without a pause (2.43 P, against 2.79 P for twice
+// the sustained 16-bit rate).  Few tiles (2560 x 9728 at 16 to 512 tokens: 17.2 ..
+// 17.7 us): a CTA's copies, 18 KB a step at some 50 bytes a cycle.  Codes, 4096 x
+// 2560 x 2560, k 7680: 121 thousand cycles the component sums, whose epilogue
+// rounds 31 million of them (the tensor cores are active in 57 % of these), 164
+// thousand the second half with its two planes (81 %); 144 us in all.
 //
 // Warp roles (per CTA): 0 TMA producer, 1 MMA issuer (even CTA of the pair),
 // 2 tensor-memory allocation, 3 TMA producer of the activations (8-bit weights

@@ -15,7 +15,7 @@
 // The weights of the first ring fill are requested before the kernel waits
 // for the one in front of it.
 //
-// 32 x 2560 x 9728 on 8-bit operands (25.4 MB): 6.5 us, 60 % of the measured
+// 32 x 2560 x 9728 on 8-bit operands (25.4 MB): 6.4 us, 61 % of the measured
 // copy rate; about 2.5 us of it is the kernel's start and the sums' way to their
 // owners, which small products are all of (32 x 1024 x 1024: 3.6 us).  Among
 // the splits whose clusters the GPU holds at once, the one of the fewest steps

@@ -13,7 +13,7 @@
 // 5.4 this way), and the first weights before the kernel waits for the one in
 // front of it, or quantises its token.
 //
-// 9728 x 2560 (24.9 MB): 5.4 us, 70 % of the measured copy rate; 2560 x 9728:
+// 9728 x 2560 (24.9 MB): 5.5 us, 69 % of the measured copy rate; 2560 x 9728:
 // 6.5 us.  Factors of 2560 x 2560, k 7680 (9.8 MB of codes): 8.4 us for both
 // halves, of which 1.5 us would be their bytes: two kernels' starts, and the
 // unpacking.  (Warp-level matrix instructions in place of the dot products fill

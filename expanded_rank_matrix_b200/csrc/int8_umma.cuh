@@ -210,7 +210,6 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uin
     EXTERND_MMA_STEP("1", ".b64 [%5]", "r"(0));
 #undef EXTERND_MMA_STEP
 }
-// the commit alone
 // The same on the pair's tile with the weights in tensor memory (`a`: 32 columns
 // of a step, 8 of an instruction's 32 bytes of K; both CTAs' at one address).
 __device__ __forceinline__ void mma_step_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
@@ -230,6 +229,7 @@ __device__ __forceinline__ void mma_step_tmem(uint32_t d, uint32_t a, uint64_t b
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accum), "r"(bar), "h"((uint16_t)3)
       : "memory");
 }
+// The commit alone.
 template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   if (PAIR)

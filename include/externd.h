@@ -271,7 +271,8 @@ int externd_ternary_apply(const uint32_t* packed_B, const uint32_t* packed_C, co
 #define EXTERND_BF16 2
 #define EXTERND_I8 3
 /* Largest inner dimension (n; k of the factored product) and largest output
- * dimension: every sum of 8-bit products below stays a 32-bit whole number. */
+ * dimension: every sum of 8-bit products below stays a 32-bit whole number, and
+ * every sum of 8-bit values and ternary entries below 2^24 (exact as fp32). */
 #define EXTERND_I8_MAX_INNER 131071
 #define EXTERND_I8_MAX_OUT (1 << 24)
 #define EXTERND_I8_MAX_ROWS (1 << 30)
