@@ -310,9 +310,9 @@ int externd_quantize_rows(const void* X, int type, int64_t ldx, int64_t rows, in
  *           externd_quantize_rows does (scratch: rows * (n + 19) bytes, 256 MiB
  *           at most; none for one row up to n = 32768),
  *           rows that are not finite as there; xscale is ignored.  EXTERND_I8:
- *           q itself, 16-byte aligned, ldx a multiple of 16 (every row, the
- *           last one too, holds ldx readable bytes; those past n do not
- *           count), with xscale [rows].
+ *           q itself, 16-byte aligned, ldx a multiple of 16 (every row holds
+ *           readable bytes up to the next multiple of 16 of n; those past n do
+ *           not count), with xscale [rows].
  *   W       [m][ldw] int8, 16-byte aligned, ldw >= n a multiple of 16 (as
  *           for X).
  *   wscale  [m] fp32; bias [m] fp32 or NULL.

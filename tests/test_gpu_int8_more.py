@@ -153,3 +153,19 @@ def test_negated_views():
     x, w = _x(2, 16, torch.float32, 6), _held(6, 16, 7)
     assert torch.equal(X.matmul_i8(x, w, bias=v), X.matmul_i8(x, w, bias=v + 0.0))
     assert torch.equal(X.matmul_i8(x, X.Quantized(w.q, v)), X.matmul_i8(x, X.Quantized(w.q, v + 0.0)))
+
+
+@pytest.mark.parametrize("t", [1, 2, 40, 700])
+def test_columns_of_a_wider_matrix(t):
+    """8-bit operands that are columns of a wider matrix, taken as they are: the
+    last row ends with its own 16 bytes, at the end of the storage."""
+    n, m, k = 61, 70, 90
+    g = _gen(t)
+    base = torch.randint(-127, 128, (t, 192), generator=g, device="cuda", dtype=torch.int8)
+    wide = torch.randint(-127, 128, (m, 160), generator=g, device="cuda", dtype=torch.int8)
+    s, ws = torch.rand(t, generator=g, device="cuda"), torch.rand(m, generator=g, device="cuda")
+    x, w = X.Quantized(base[:, 128:128 + n], s), X.Quantized(wide[:, 96:96 + n], ws)
+    assert x.q.data_ptr() == base.data_ptr() + 128 and w.q.data_ptr() == wide.data_ptr() + 96
+    R.check(X.matmul_i8(x, w), *R.dense(x.q, s, w.q, ws))
+    f, B, C, D = _factors(m, n, k, 3)
+    R.check(X.apply_i8(X.pack_codes(f), x), *R.factors(x.q.double(), s, B, C, D))
